@@ -1,0 +1,727 @@
+// ffn_api.cu -- the C ABI of the feed-forward operators (include/tsffn.h):
+// handles, argument checks, and the launches of the products on the GEMM
+// kernels with (or, in the backward passes, without) a feed-forward epilogue.
+//
+// Tensor maps are encoded anew by every call; of a problem only its
+// configuration (tile, schedule, grid) is kept, by its sizes and types.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <new>
+#include <tuple>
+#include <vector>
+
+#include "ffn_kernels.h"
+#include "gemm_sm103.cuh"
+#include "kernels.h"
+#include "planner.h"
+#include "tsffn.h"
+
+namespace {
+
+using tsg::FfnEpilogue;
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+        else
+            (void)cudaGetLastError();
+    });
+    return fn;
+}
+
+// tcgen05 kind::f16 instruction descriptor (see tsgemm_api.cu's make_idesc).
+uint32_t make_idesc(bool bf16, int m, int n, int layout) {
+    const uint32_t fmt = bf16 ? 1u : 0u;
+    const uint32_t a_mn = tsg::a_kmajor(layout) ? 0u : 1u;
+    const uint32_t b_mn = tsg::b_kmajor(layout) ? 0u : 1u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (a_mn << 15) | (b_mn << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+int64_t elem_bytes(int dt) { return dt == TSGEMM_F32 ? 4 : 2; }
+int out_kind(int dt) {
+    return dt == TSGEMM_F16 ? tsg::kOutF16 : (dt == TSGEMM_BF16 ? tsg::kOutBF16 : tsg::kOutF32);
+}
+int elem_kind(int dt) {
+    return dt == TSGEMM_F16 ? tsg::kElemF16 : (dt == TSGEMM_BF16 ? tsg::kElemBF16 : tsg::kElemF32);
+}
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+
+constexpr int64_t kLimit = (int64_t{1} << 31) - 1;
+constexpr int64_t kWorkspaceBytes = int64_t{64} << 20;  // split-K / stream-K partials, or column sums
+constexpr int64_t kCounters = 65536;
+constexpr int64_t kClipPartials = 16384;
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+
+}  // namespace
+
+// The configuration of a product: which kernel, tile, schedule and grid.
+struct FfnConfig {
+    tsgemm_config_t cfg;
+    const void* kernel;
+    int64_t smem;
+};
+
+struct tsffn_s {
+    int device;
+    int num_sms;
+    float* ws;
+    int* counters;
+    int* clip_counter;
+    double* clip_partials;
+    float* clip_coef;
+    int* status;
+    std::mutex mu;  // the configurations
+    std::map<std::tuple<int, int64_t, int64_t, int64_t, int, int, int>, FfnConfig> configs;
+};
+
+namespace {
+
+void handle_free(tsffn_s* h) {
+    if (!h) return;
+    if (h->ws) cudaFree(h->ws);
+    if (h->counters) cudaFree(h->counters);
+    if (h->clip_partials) cudaFree(h->clip_partials);
+    delete h;
+}
+
+const void* kernel_of(int kind, int layout, const tsgemm_config_t& c, int out) {
+    const bool pair = c.block_m == 256;
+    if (kind == tsg::kEpiPlain)
+        return pair ? tsg::kernel_2sm(c.block_n, out, layout, false) : tsg::kernel_1sm(c.block_n, out, layout, false, 1);
+    const int n = c.block_n;
+    if (kind == tsg::kEpiLinear) {
+        switch (layout) {
+            case 0: return pair ? tsg::kernel_linear_2sm_layout0(n, out) : tsg::kernel_linear_1sm_layout0(n, out);
+            case 1: return pair ? tsg::kernel_linear_2sm_layout1(n, out) : tsg::kernel_linear_1sm_layout1(n, out);
+            case 2: return pair ? tsg::kernel_linear_2sm_layout2(n, out) : tsg::kernel_linear_1sm_layout2(n, out);
+            default: return nullptr;
+        }
+    }
+    switch (layout) {
+        case 0: return pair ? tsg::kernel_gated_2sm_layout0(n, out) : tsg::kernel_gated_1sm_layout0(n, out);
+        case 1: return pair ? tsg::kernel_gated_2sm_layout1(n, out) : tsg::kernel_gated_1sm_layout1(n, out);
+        default: return nullptr;
+    }
+}
+
+int64_t counters_of(const tsgemm_config_t& c) {
+    return (c.stream_k_tiles > 0 ? c.stream_k_tiles : c.split_tiles) * (c.block_m / 128) * (c.block_n / 32) * 4;
+}
+
+// The configuration for a product of M x N x K (gated: N = 2 F).  The
+// planner's sizes are rounded up to its own rule on row strides, which
+// changes neither tiles nor K slices.
+tsgemm_status_t make_config(tsffn_s* h, int kind, int64_t M, int64_t N, int64_t K, int din, int dout, int layout,
+                            FfnConfig* out) {
+    const auto key = std::make_tuple(kind, M, N, K, din, dout, layout);
+    std::lock_guard<std::mutex> lock(h->mu);
+    const auto it = h->configs.find(key);
+    if (it != h->configs.end()) {
+        *out = it->second;
+        return TSGEMM_OK;
+    }
+    const unsigned widths = kind == tsg::kEpiGated ? tsg::kGatedWidths : tsg::kAllWidths;
+    const int64_t Mp = tsg::a_kmajor(layout) ? M : round8(M);
+    FfnConfig f{};
+    tsgemm_status_t st =
+        tsg::choose_config(Mp, round8(N), round8(K), din, dout, layout, h->num_sms, nullptr, &f.cfg, widths);
+    if (st != TSGEMM_OK) return st;
+    if (f.cfg.workspace_bytes > kWorkspaceBytes || counters_of(f.cfg) > kCounters) {
+        tsgemm_config_t whole{};
+        whole.splits = 1;
+        whole.stream_k_tiles = -1;
+        st = tsg::choose_config(Mp, round8(N), round8(K), din, dout, layout, h->num_sms, &whole, &f.cfg, widths);
+        if (st != TSGEMM_OK) return st;
+    }
+    const bool pair = f.cfg.block_m == 256;
+    f.kernel = kernel_of(kind, layout, f.cfg, out_kind(dout));
+    const int64_t need = tsg::smem_bytes_for(f.cfg.block_m, f.cfg.block_n, dout, f.cfg.stages, 1);
+    if (!f.kernel || need > tsg::kSmemPerCtaMax) return TSGEMM_ERR_UNSUPPORTED;
+    // (more than half the SM's shared memory, so one CTA owns each SM and
+    // its tensor memory)
+    f.smem = std::max<int64_t>(need, tsg::kSmemPerCtaMax / 2 + 1024);
+    if (cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(tsg::kSmemPerCtaMax)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
+    }
+    if (pair) {
+        // persistent clusters: no more than can be resident at once
+        cudaLaunchConfig_t lc{};
+        lc.gridDim = dim3(static_cast<unsigned>(f.cfg.grid), 1, 1);
+        lc.blockDim = dim3(tsg::kThreads, 1, 1);
+        lc.dynamicSmemBytes = static_cast<size_t>(f.smem);
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, f.kernel, &lc) != cudaSuccess || clusters < 1) {
+            (void)cudaGetLastError();
+            return TSGEMM_ERR_UNSUPPORTED;
+        }
+        if (f.cfg.grid > 2 * clusters) f.cfg.grid = 2 * clusters;
+    }
+    if (h->configs.size() >= 4096) h->configs.clear();
+    h->configs.emplace(key, f);
+    *out = f;
+    return TSGEMM_OK;
+}
+
+struct Product {
+    int kind;         // EpiKind
+    int64_t M, N, K;  // of the product (gated: N = 2 F)
+    int din, dout, layout;
+    const void* A;
+    const void* B;
+    void* C;
+    int64_t lda, ldb, ldc;
+    FfnEpilogue epi;
+};
+
+tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
+    FfnConfig f;
+    const tsgemm_status_t st = make_config(h, g.kind, g.M, g.N, g.K, g.din, g.dout, g.layout, &f);
+    if (st != TSGEMM_OK) return st;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return TSGEMM_ERR_CUDA;
+    const tsgemm_config_t& c = f.cfg;
+    const bool pair = c.block_m == 256, gated = g.kind == tsg::kEpiGated;
+    const int64_t n_out = gated ? g.N / 2 : g.N;       // columns of C
+    const int64_t tile_out = gated ? c.block_n / 2 : c.block_n;
+
+    alignas(64) CUtensorMap tmA, tmB, tmC;
+    const cuuint32_t estr[2] = {1, 1};
+    auto map = [&](CUtensorMap* m, int dt, const void* p, int64_t inner, int64_t outer, int64_t ld, cuuint32_t bi,
+                   cuuint32_t bo, CUtensorMapSwizzle sw, CUtensorMapL2promotion prom) {
+        const CUtensorMapDataType t = dt == TSGEMM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                      : dt == TSGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * elem_bytes(dt))};
+        const cuuint32_t box[2] = {bi, bo};
+        return enc(m, t, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, prom,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    // operand boxes and L2 fills as tsgemm_run's; a gated layer's B comes in
+    // two boxes (gate and up columns) of half the tile each
+    const CUtensorMapL2promotion prom = pair ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    const cuuint32_t b_cols = static_cast<cuuint32_t>(
+        pair ? (c.block_n == 512 ? 128 : c.block_n / 2) : (gated ? c.block_n / 2 : c.block_n));
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const bool ok_a = tsg::a_kmajor(g.layout) ? map(&tmA, g.din, g.A, g.K, g.M, g.lda, 64, 128, sw, prom)
+                                              : map(&tmA, g.din, g.A, g.M, g.K, g.lda, 64, 64, sw, prom);
+    const bool ok_b = tsg::b_kmajor(g.layout) ? map(&tmB, g.din, g.B, g.K, g.N, g.ldb, 64, b_cols, sw, prom)
+                                              : map(&tmB, g.din, g.B, g.N, g.K, g.ldb, 64, 64, sw, prom);
+    const bool ok_c = map(&tmC, g.dout, g.C, n_out, g.M, g.ldc, 32, 32,
+                          g.dout == TSGEMM_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    if (!ok_a || !ok_b || !ok_c) return TSGEMM_ERR_CUDA;
+
+    tsg::FfnParams p{};
+    p.M = static_cast<int32_t>(g.M);
+    p.N = static_cast<int32_t>(n_out);
+    p.K = static_cast<int32_t>(g.K);
+    p.tiles_m = static_cast<int32_t>((g.M + c.block_m - 1) / c.block_m);
+    p.tiles_n = static_cast<int32_t>((n_out + tile_out - 1) / tile_out);
+    p.splits = c.splits;
+    p.kblocks = static_cast<int32_t>((g.K + tsg::kBK - 1) / tsg::kBK);
+    p.group_m = c.group_m;
+    p.stages = c.stages;
+    p.units = c.units;
+    p.full_tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n - c.split_tiles - c.stream_k_tiles;
+    p.sk_tiles = c.stream_k_tiles;
+    p.sk_work = c.stream_k_tiles * p.kblocks;
+    p.idesc = make_idesc(g.din == TSGEMM_BF16, c.block_m, c.block_n == 512 ? 256 : c.block_n, g.layout);
+    p.csplit = 1;
+    p.C = g.C;
+    p.ws = h->ws;
+    p.ws_own = c.stream_k_tiles > 0 ? h->ws + static_cast<int64_t>(c.grid) * 128 * c.block_n : nullptr;
+    p.counters = h->counters;
+    p.status = h->status;
+    p.timeout_ns = kTimeoutNs;
+    p.epi = g.epi;
+
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(c.grid), 1, 1);
+    lc.blockDim = dim3(tsg::kThreads, 1, 1);
+    lc.dynamicSmemBytes = static_cast<size_t>(f.smem);
+    lc.stream = stream;
+    // (a plain kernel takes the GemmParams that FfnParams begins with)
+    void* args[4] = {&tmA, &tmB, &tmC, &p};
+    if (cudaLaunchKernelExC(&lc, f.kernel, args) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
+    }
+    return TSGEMM_OK;
+}
+
+// ------------------------------------------------------ argument checks --
+
+// A rows x cols matrix of elements of `e` bytes, rows `ld` elements apart.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;
+    int64_t e;
+    int64_t bytes() const { return ((rows - 1) * ld + cols) * e; }
+};
+
+// True when the two share memory.  Ranges of addresses that cross are told
+// apart when both have the same row stride in bytes and their columns never
+// meet (column slices of one buffer).
+bool overlaps(const Mat& a, const Mat& b) {
+    if (!a.p || !b.p) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    if (x >= y + static_cast<uintptr_t>(b.bytes()) || y >= x + static_cast<uintptr_t>(a.bytes())) return false;
+    const int64_t la = a.ld * a.e, lb = b.ld * b.e;
+    if (la == lb && a.rows > 1 && b.rows > 1) {
+        int64_t d = static_cast<int64_t>(y - x) % la;  // where b's columns begin in a's rows
+        if (d < 0) d += la;
+        return !(d >= a.cols * a.e && d + b.cols * b.e <= la);
+    }
+    return true;
+}
+
+// Address and stride alignment, and a stride that holds the row.
+tsgemm_status_t check_mat(const Mat& m) {
+    if (m.ld < m.cols) return TSGEMM_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(m.p) & 15u) != 0 || (m.ld * m.e) % 16 != 0) return TSGEMM_ERR_ALIGNMENT;
+    // (addresses are formed in 64 bits; a tensor map's stride is 40 bits)
+    if (m.ld > kLimit || m.rows > (int64_t{1} << 60) / (m.ld * m.e)) return TSGEMM_ERR_UNSUPPORTED;
+    return TSGEMM_OK;
+}
+
+// Sizes before anything is computed from them.
+tsgemm_status_t check_sizes(int64_t M, int64_t N, int64_t K) {
+    if (M < 1 || N < 1 || K < 1) return TSGEMM_ERR_INVALID_ARG;
+    return M > kLimit || N > kLimit || K > kLimit ? TSGEMM_ERR_UNSUPPORTED : TSGEMM_OK;
+}
+// The gated layer's: the product has 2 F columns, and the up half begins on
+// a 16-byte boundary.
+tsgemm_status_t check_gated_sizes(int64_t M, int64_t F, int64_t K) {
+    const tsgemm_status_t st = check_sizes(M, F, K);
+    if (st != TSGEMM_OK) return st;
+    if (2 * F > kLimit) return TSGEMM_ERR_UNSUPPORTED;
+    return F % 8 == 0 ? TSGEMM_OK : TSGEMM_ERR_ALIGNMENT;
+}
+
+tsgemm_status_t check_device(const tsffn_s* h) {
+    if (!h) return TSGEMM_ERR_INVALID_ARG;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
+    }
+    return dev == h->device ? TSGEMM_OK : TSGEMM_ERR_INVALID_ARG;
+}
+
+tsgemm_status_t check_device_ptr(const void* p, int device) {
+    cudaPointerAttributes a{};
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_INVALID_ARG;
+    }
+    if (a.type == cudaMemoryTypeManaged) return TSGEMM_OK;
+    return a.type == cudaMemoryTypeDevice && a.device == device ? TSGEMM_OK : TSGEMM_ERR_INVALID_ARG;
+}
+
+// The checks that the four matrix entry points share, host only (they come
+// before the handle is looked at): types, the matrices that are present
+// (inputs first, then outputs), no output on anything else (but `alias`,
+// which may be the first output exactly).
+struct Call {
+    int dtype, layout, act;
+    std::vector<Mat> in, out;
+    Mat alias{};  // present when .p is set
+};
+
+tsgemm_status_t check_call(const Call& c) {
+    if (c.act < TSFFN_ACT_NONE || c.act > TSFFN_ACT_SIGMOID) return TSGEMM_ERR_INVALID_ARG;
+    if (c.layout < TSGEMM_LAYOUT_RRR || c.layout > TSGEMM_LAYOUT_CCR) return TSGEMM_ERR_INVALID_ARG;
+    if (c.dtype < TSGEMM_F16 || c.dtype > TSGEMM_E5M2) return TSGEMM_ERR_INVALID_ARG;
+    if (c.dtype != TSGEMM_F16 && c.dtype != TSGEMM_BF16) return TSGEMM_ERR_UNSUPPORTED;
+    if (c.layout != TSGEMM_LAYOUT_RRR && c.layout != TSGEMM_LAYOUT_RCR) return TSGEMM_ERR_UNSUPPORTED;
+    for (const auto* list : {&c.in, &c.out})
+        for (const Mat& m : *list)
+            if (m.p) {
+                const tsgemm_status_t st = check_mat(m);
+                if (st != TSGEMM_OK) return st;
+            }
+    if (c.alias.p) {
+        const tsgemm_status_t st = check_mat(c.alias);
+        if (st != TSGEMM_OK) return st;
+    }
+    for (size_t i = 0; i < c.out.size(); ++i) {
+        for (const Mat& m : c.in)
+            if (overlaps(c.out[i], m)) return TSGEMM_ERR_INVALID_ARG;
+        for (size_t j = 0; j < i; ++j)
+            if (overlaps(c.out[i], c.out[j])) return TSGEMM_ERR_INVALID_ARG;
+        const bool same = i == 0 && c.alias.p == c.out[0].p && c.alias.ld == c.out[0].ld;
+        if (!same && overlaps(c.out[i], c.alias)) return TSGEMM_ERR_INVALID_ARG;
+    }
+    return TSGEMM_OK;
+}
+
+// The handle is of the current device, and so is every matrix.
+tsgemm_status_t check_memory(const tsffn_s* h, const Call& c) {
+    tsgemm_status_t st = check_device(h);
+    if (st != TSGEMM_OK) return st;
+    for (const auto* list : {&c.in, &c.out})
+        for (const Mat& m : *list)
+            if (m.p && (st = check_device_ptr(m.p, h->device)) != TSGEMM_OK) return st;
+    if (c.alias.p) st = check_device_ptr(c.alias.p, h->device);
+    return st;
+}
+
+// dtype or fp32
+tsgemm_status_t check_out_type(int dt, int dtype) {
+    if (dt < TSGEMM_F16 || dt > TSGEMM_E5M2) return TSGEMM_ERR_INVALID_ARG;
+    return dt == dtype || dt == TSGEMM_F32 ? TSGEMM_OK : TSGEMM_ERR_UNSUPPORTED;
+}
+
+Mat weights(const void* W, int layout, int64_t N, int64_t K, int64_t ldw, int64_t e) {
+    return layout == TSGEMM_LAYOUT_RCR ? Mat{W, N, K, ldw, e} : Mat{W, K, N, ldw, e};
+}
+
+// A product without an epilogue, into C of any width and stride: the plain
+// kernels where they can store it (rows of whole 16-byte pieces, fp32 rows
+// dense), else the linear layer's with nothing to do.
+Product plain_product(int64_t M, int64_t N, int64_t K, int din, int dout, int layout, const void* A, int64_t lda,
+                      const void* B, int64_t ldb, void* C, int64_t ldc) {
+    FfnEpilogue e{};
+    e.ldc = ldc;
+    const bool plain = dout == TSGEMM_F32 ? ldc == N : N % 8 == 0;
+    return Product{plain ? tsg::kEpiPlain : tsg::kEpiLinear, M, N, K, din, dout, layout, A, B, C, lda, ldb, ldc, e};
+}
+
+// dX (M x K) = D W^T and dW = X^T D, D (M x N) 16-bit.
+tsgemm_status_t run_backward(tsffn_s* h, int64_t M, int64_t N, int64_t K, int dtype, int dtype_dw, int layout,
+                             const void* D, int64_t ldd, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                             void* dX, int64_t lddx, void* dW, int64_t lddw, cudaStream_t s) {
+    const bool rcr = layout == TSGEMM_LAYOUT_RCR;
+    if (dX) {
+        // W^T (N x K) is stored K x N when W is (its N x K form: RCR), and
+        // N x K when W is (RRR)
+        const tsgemm_status_t st = run_product(
+            h, plain_product(M, K, N, dtype, dtype, rcr ? TSGEMM_LAYOUT_RRR : TSGEMM_LAYOUT_RCR, D, ldd, W, ldw, dX, lddx),
+            s);
+        if (st != TSGEMM_OK) return st;
+    }
+    if (!dW) return TSGEMM_OK;
+    return run_product(
+        h, rcr ? plain_product(N, K, M, dtype, dtype_dw, TSGEMM_LAYOUT_CRR, D, ldd, X, ldx, dW, lddw)
+               : plain_product(K, N, M, dtype, dtype_dw, TSGEMM_LAYOUT_CRR, X, ldx, D, ldd, dW, lddw), s);
+}
+
+tsgemm_status_t cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return TSGEMM_OK;
+    (void)cudaGetLastError();
+    return TSGEMM_ERR_CUDA;
+}
+
+// counters | clip counter | status word
+constexpr size_t kWords = static_cast<size_t>(kCounters) + 2;
+
+tsgemm_status_t allocate(tsffn_s* h) {
+    if (cudaMalloc(&h->ws, static_cast<size_t>(kWorkspaceBytes)) != cudaSuccess ||
+        cudaMalloc(&h->counters, kWords * sizeof(int)) != cudaSuccess ||
+        cudaMalloc(&h->clip_partials, (kClipPartials + 1) * sizeof(double)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_OOM;
+    }
+    cudaStream_t s = nullptr;
+    bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+    ok = ok && cudaMemsetAsync(h->counters, 0, kWords * sizeof(int), s) == cudaSuccess &&
+         cudaStreamSynchronize(s) == cudaSuccess;
+    if (s) (void)cudaStreamDestroy(s);
+    if (!ok) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
+    }
+    h->clip_counter = h->counters + kCounters;
+    h->status = h->counters + kCounters + 1;
+    h->clip_coef = reinterpret_cast<float*>(h->clip_partials + kClipPartials);
+    return TSGEMM_OK;
+}
+
+// No exception leaves a C entry point (the containers here may throw).
+template <class F>
+tsgemm_status_t guarded(F&& f) {
+    try {
+        return f();
+    } catch (const std::bad_alloc&) {
+        return TSGEMM_ERR_OOM;
+    } catch (...) {
+        return TSGEMM_ERR_CUDA;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+tsgemm_status_t tsffn_create(tsffn_t* out) {
+    if (!out) return TSGEMM_ERR_INVALID_ARG;
+    *out = nullptr;
+    int dev = 0, major = 0, minor = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
+    }
+    if (major != 10 || minor != 3) return TSGEMM_ERR_UNSUPPORTED;
+    if (!encode_fn()) return TSGEMM_ERR_CUDA;
+    return guarded([&] {
+        tsffn_s* h = new (std::nothrow) tsffn_s();
+        if (!h) return TSGEMM_ERR_OOM;
+        h->device = dev;
+        h->num_sms = sms;
+        // (a handle may be made while another stream of this thread is being
+        // captured: allocations are allowed then in the relaxed mode, and the
+        // zeroing runs on a stream of its own)
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        (void)cudaThreadExchangeStreamCaptureMode(&mode);
+        const tsgemm_status_t st = allocate(h);
+        (void)cudaThreadExchangeStreamCaptureMode(&mode);
+        if (st != TSGEMM_OK) {
+            handle_free(h);
+            return st;
+        }
+        *out = h;
+        return TSGEMM_OK;
+    });
+}
+
+tsgemm_status_t tsffn_destroy(tsffn_t handle) {
+    handle_free(handle);
+    return TSGEMM_OK;
+}
+
+tsgemm_status_t tsffn_status(tsffn_t h) {
+    if (!h) return TSGEMM_ERR_INVALID_ARG;
+    int word = 0;
+    if (cudaMemcpy(&word, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
+    }
+    if (word == TSGEMM_OK) return TSGEMM_OK;
+    // a run gave up: the counters it left behind start from zero again
+    if (cudaMemset(h->counters, 0, kWords * sizeof(int)) != cudaSuccess ||
+        cudaDeviceSynchronize() != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
+    }
+    return static_cast<tsgemm_status_t>(word);
+}
+
+tsgemm_status_t tsffn_linear(tsffn_t h, const tsffn_linear_args* a, void* stream) {
+    if (!a || !a->X || !a->W || !a->C || a->reserved != 0) return TSGEMM_ERR_INVALID_ARG;
+    const tsgemm_status_t sizes = check_sizes(a->M, a->N, a->K);
+    if (sizes != TSGEMM_OK) return sizes;
+    return guarded([&]() -> tsgemm_status_t {
+        const int64_t eo = elem_bytes(a->dtype_out), eb = elem_bytes(a->dtype_bias);
+        Call c{a->dtype, a->layout, a->act, {}, {}, {}};
+        c.in = {{a->X, a->M, a->K, a->ldx, 2},
+                weights(a->W, a->layout, a->N, a->K, a->ldw, 2),
+                {a->bias, 1, a->N, round8(a->N), eb}};
+        c.out = {{a->C, a->M, a->N, a->ldc, eo}, {a->saved, a->M, a->N, TSFFN_SAVED_LD(a->N), 4}};
+        if (a->residual) c.alias = {a->residual, a->M, a->N, a->ldr, eo};
+        tsgemm_status_t st = check_call(c);
+        if (st == TSGEMM_OK) st = check_out_type(a->dtype_out, a->dtype);
+        if (st == TSGEMM_OK && a->bias) st = check_out_type(a->dtype_bias, a->dtype);
+        if (st == TSGEMM_OK) st = check_memory(h, c);
+        if (st != TSGEMM_OK) return st;
+        FfnEpilogue e{};
+        e.bias = a->bias;
+        e.bias_kind = a->bias ? elem_kind(a->dtype_bias) : tsg::kElemNone;
+        e.residual = a->residual;
+        e.ldr = a->ldr;
+        e.saved = a->saved;
+        e.lds = TSFFN_SAVED_LD(a->N);
+        e.ldc = a->ldc;
+        e.act = a->act;
+        const Product g{tsg::kEpiLinear, a->M, a->N, a->K, a->dtype, a->dtype_out, a->layout,
+                        a->X, a->W, a->C, a->ldx, a->ldw, a->ldc, e};
+        return run_product(h, g, static_cast<cudaStream_t>(stream));
+    });
+}
+
+tsgemm_status_t tsffn_linear_backward(tsffn_t h, const tsffn_linear_backward_args* a, void* stream) {
+    if (!a || !a->dC || a->reserved != 0) return TSGEMM_ERR_INVALID_ARG;
+    if ((a->dX && !a->W) || (a->dW && !a->X)) return TSGEMM_ERR_INVALID_ARG;
+    const bool grad = a->act != TSFFN_ACT_NONE;
+    const bool products = a->dX || a->dW;
+    if (!products && !a->dbias) return TSGEMM_ERR_INVALID_ARG;
+    if (grad && (!a->saved || (products && !a->workspace))) return TSGEMM_ERR_INVALID_ARG;
+    const tsgemm_status_t sizes = check_sizes(a->M, a->N, a->K);
+    if (sizes != TSGEMM_OK) return sizes;
+    return guarded([&]() -> tsgemm_status_t {
+        const int64_t ldz = TSFFN_SAVED_LD(a->N);
+        Call c{a->dtype, a->layout, a->act, {}, {}, {}};
+        c.in = {{a->dC, a->M, a->N, a->lddc, 2}};
+        if (a->dW) c.in.push_back({a->X, a->M, a->K, a->ldx, 2});
+        if (a->dX) c.in.push_back(weights(a->W, a->layout, a->N, a->K, a->ldw, 2));
+        if (grad) c.in.push_back({a->saved, a->M, a->N, ldz, 4});
+        const Mat dw = weights(a->dW, a->layout, a->N, a->K, a->lddw, elem_bytes(a->dtype_dw));
+        c.out = {{a->dX, a->M, a->K, a->lddx, 2},
+                 dw,
+                 {a->dbias, 1, a->N, ldz, elem_bytes(a->dtype_bias)},
+                 {grad && products ? a->workspace : nullptr, a->M, a->N, ldz, 2}};
+        tsgemm_status_t st = check_call(c);
+        if (st == TSGEMM_OK && a->dW) st = check_out_type(a->dtype_dw, a->dtype);
+        if (st == TSGEMM_OK && a->dbias) st = check_out_type(a->dtype_bias, a->dtype);
+        if (st == TSGEMM_OK) st = check_memory(h, c);
+        if (st != TSGEMM_OK) return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const void* D = a->dC;
+        int64_t ldd = a->lddc;
+        if (a->dbias || (grad && products)) {
+            tsg::LinearGradArgs g{};
+            g.M = a->M;
+            g.N = a->N;
+            g.bf16 = a->dtype == TSGEMM_BF16;
+            g.act = a->act;
+            g.dC = a->dC;
+            g.lddc = a->lddc;
+            g.saved = a->saved;
+            g.lds = ldz;
+            g.dZ = grad && products ? a->workspace : nullptr;
+            g.ldz = ldz;
+            g.dbias = a->dbias;
+            g.dbias_f32 = a->dtype_bias == TSGEMM_F32;
+            const tsg::ColumnSums sums{h->ws, kWorkspaceBytes / 4, h->counters, kCounters};
+            st = cuda_status(tsg::launch_linear_grad(g, sums, h->num_sms, s));
+            if (st != TSGEMM_OK) return st;
+            if (g.dZ) {
+                D = g.dZ;
+                ldd = ldz;
+            }
+        }
+        return run_backward(h, a->M, a->N, a->K, a->dtype, a->dtype_dw, a->layout, D, ldd, a->X, a->ldx, a->W, a->ldw,
+                            a->dX, a->lddx, a->dW, a->lddw, s);
+    });
+}
+
+tsgemm_status_t tsffn_gated(tsffn_t h, const tsffn_gated_args* a, void* stream) {
+    if (!a || !a->X || !a->W || !a->H || a->reserved != 0) return TSGEMM_ERR_INVALID_ARG;
+    const tsgemm_status_t sizes = check_gated_sizes(a->M, a->F, a->K);
+    if (sizes != TSGEMM_OK) return sizes;
+    return guarded([&]() -> tsgemm_status_t {
+        Call c{a->dtype, a->layout, a->act, {}, {}, {}};
+        c.in = {{a->X, a->M, a->K, a->ldx, 2}, weights(a->W, a->layout, 2 * a->F, a->K, a->ldw, 2)};
+        c.out = {{a->H, a->M, a->F, a->ldh, 2}, {a->saved, a->M, 2 * a->F, 2 * a->F, 4}};
+        tsgemm_status_t st = check_call(c);
+        if (st == TSGEMM_OK) st = check_memory(h, c);
+        if (st != TSGEMM_OK) return st;
+        FfnEpilogue e{};
+        e.saved = a->saved;
+        e.lds = 2 * a->F;
+        e.ldc = a->ldh;
+        e.act = a->act;
+        const Product g{tsg::kEpiGated, a->M, 2 * a->F, a->K, a->dtype, a->dtype, a->layout,
+                        a->X, a->W, a->H, a->ldx, a->ldw, a->ldh, e};
+        return run_product(h, g, static_cast<cudaStream_t>(stream));
+    });
+}
+
+tsgemm_status_t tsffn_gated_backward(tsffn_t h, const tsffn_gated_backward_args* a, void* stream) {
+    if (!a || !a->dH || !a->saved || !a->workspace) return TSGEMM_ERR_INVALID_ARG;
+    if ((a->dX && !a->W) || (a->dW && !a->X) || (!a->dX && !a->dW)) return TSGEMM_ERR_INVALID_ARG;
+    const tsgemm_status_t sizes = check_gated_sizes(a->M, a->F, a->K);
+    if (sizes != TSGEMM_OK) return sizes;
+    return guarded([&]() -> tsgemm_status_t {
+        const int64_t N = 2 * a->F;
+        Call c{a->dtype, a->layout, a->act, {}, {}, {}};
+        c.in = {{a->dH, a->M, a->F, a->lddh, 2}, {a->saved, a->M, N, N, 4}};
+        if (a->dW) c.in.push_back({a->X, a->M, a->K, a->ldx, 2});
+        if (a->dX) c.in.push_back(weights(a->W, a->layout, N, a->K, a->ldw, 2));
+        const Mat dw = weights(a->dW, a->layout, N, a->K, a->lddw, elem_bytes(a->dtype_dw));
+        c.out = {{a->dX, a->M, a->K, a->lddx, 2}, dw, {a->workspace, a->M, N, N, 2}};
+        tsgemm_status_t st = check_call(c);
+        if (st == TSGEMM_OK && a->dW) st = check_out_type(a->dtype_dw, a->dtype);
+        if (st == TSGEMM_OK) st = check_memory(h, c);
+        if (st != TSGEMM_OK) return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        tsg::GatedGradArgs g{};
+        g.M = a->M;
+        g.F = a->F;
+        g.bf16 = a->dtype == TSGEMM_BF16;
+        g.act = a->act;
+        g.dH = a->dH;
+        g.lddh = a->lddh;
+        g.saved = a->saved;
+        g.dGU = a->workspace;
+        st = cuda_status(tsg::launch_gated_grad(g, h->num_sms, s));
+        if (st != TSGEMM_OK) return st;
+        return run_backward(h, a->M, N, a->K, a->dtype, a->dtype_dw, a->layout, a->workspace, N, a->X, a->ldx, a->W,
+                            a->ldw, a->dX, a->lddx, a->dW, a->lddw, s);
+    });
+}
+
+tsgemm_status_t tsffn_clip_grad_norm(tsffn_t h, int64_t count, const void* const* grads, void* const* out,
+                                     const int64_t* numel, const int32_t* dtype, float max_norm, float* norm,
+                                     void* stream) {
+    if (count < 0 || !norm || !(max_norm >= 0.0f)) return TSGEMM_ERR_INVALID_ARG;
+    if (count > 0 && (!grads || !out || !numel || !dtype)) return TSGEMM_ERR_INVALID_ARG;
+    return guarded([&]() -> tsgemm_status_t {
+        // [begin, end) of every output and of every input that is not its
+        // own output; an output may meet nothing else
+        struct Range {
+            uintptr_t begin, end;
+            bool out;
+        };
+        std::vector<Range> ranges;
+        ranges.reserve(static_cast<size_t>(2 * count + 1));
+        for (int64_t i = 0; i < count; ++i) {
+            if (numel[i] < 0) return TSGEMM_ERR_INVALID_ARG;
+            if (dtype[i] < TSGEMM_F16 || dtype[i] > TSGEMM_E5M2) return TSGEMM_ERR_INVALID_ARG;
+            if (dtype[i] > TSGEMM_F32) return TSGEMM_ERR_UNSUPPORTED;
+            if (numel[i] == 0) continue;
+            if (!grads[i] || !out[i]) return TSGEMM_ERR_INVALID_ARG;
+            const uintptr_t e = static_cast<uintptr_t>(elem_bytes(dtype[i]));
+            const uintptr_t x = reinterpret_cast<uintptr_t>(grads[i]), y = reinterpret_cast<uintptr_t>(out[i]);
+            if ((x | y) & (e - 1)) return TSGEMM_ERR_ALIGNMENT;
+            ranges.push_back({y, y + e * static_cast<uintptr_t>(numel[i]), true});
+            if (x != y) ranges.push_back({x, x + e * static_cast<uintptr_t>(numel[i]), false});
+        }
+        const uintptr_t nw = reinterpret_cast<uintptr_t>(norm);
+        if (nw & 3u) return TSGEMM_ERR_ALIGNMENT;
+        ranges.push_back({nw, nw + sizeof(float), true});
+        std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
+        // furthest ends so far, of outputs and of all ranges
+        uintptr_t out_end = 0, any_end = 0;
+        for (const Range& r : ranges) {
+            if (r.begin < out_end || (r.out && r.begin < any_end)) return TSGEMM_ERR_INVALID_ARG;
+            any_end = std::max(any_end, r.end);
+            if (r.out) out_end = std::max(out_end, r.end);
+        }
+        tsgemm_status_t st = check_device(h);  // (from here on the device is asked)
+        if (st == TSGEMM_OK) st = check_device_ptr(norm, h->device);
+        for (int64_t i = 0; i < count && st == TSGEMM_OK; ++i) {
+            if (numel[i] == 0) continue;
+            st = check_device_ptr(grads[i], h->device);
+            if (st == TSGEMM_OK && out[i] != grads[i]) st = check_device_ptr(out[i], h->device);
+        }
+        if (st != TSGEMM_OK) return st;
+        const tsg::ClipScratch scratch{h->clip_partials, kClipPartials, h->clip_counter, h->clip_coef};
+        return cuda_status(tsg::launch_clip(count, grads, out, numel, dtype, max_norm, norm, scratch, h->num_sms,
+                                            static_cast<cudaStream_t>(stream)));
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,63 @@
+// ffn_kernels.h -- launches of the feed-forward operators' own kernels (the
+// products themselves run on the GEMM kernels of kernels.h).  Arguments are
+// checked by the callers; each function enqueues on `stream` and returns the
+// launch's status.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace tsg {
+
+// Column sums that several CTAs make together: fp32 partials
+// [row chunk][columns], and one arrival counter per strip of columns (zero
+// between launches).
+struct ColumnSums {
+    float* partials;
+    int64_t partial_floats;
+    int* counters;
+    int64_t num_counters;
+};
+
+// dZ = dC * act'(Z) (16-bit, rows ldz apart, unless dZ is null) and, unless
+// dbias is null, its column sums.  saved: Z, rows lds apart (act none: not
+// read).
+struct LinearGradArgs {
+    int64_t M, N;
+    bool bf16;
+    int act;
+    const void* dC;
+    const float* saved;
+    void* dZ;
+    void* dbias;
+    bool dbias_f32;
+    int64_t lddc, lds, ldz;
+};
+cudaError_t launch_linear_grad(const LinearGradArgs& a, const ColumnSums& sums, int num_sms, cudaStream_t stream);
+
+// dGU = [dH * U * act'(G), dH * act(G)] (16-bit, rows 2 F apart) from
+// saved = [G U] (fp32, rows 2 F apart).  F a multiple of 8.
+struct GatedGradArgs {
+    int64_t M, F;
+    bool bf16;
+    int act;
+    const void* dH;
+    const float* saved;
+    void* dGU;
+    int64_t lddh;
+};
+cudaError_t launch_gated_grad(const GatedGradArgs& a, int num_sms, cudaStream_t stream);
+
+// Scratch of the global norm: one fp64 partial per thread block, a counter
+// (zero between launches) and the coefficient the scaling pass reads.
+struct ClipScratch {
+    double* partials;
+    int64_t max_partials;
+    int* counter;
+    float* coef;
+};
+cudaError_t launch_clip(int64_t count, const void* const* grads, void* const* out, const int64_t* numel,
+                        const int32_t* dtype, float max_norm, float* norm, const ClipScratch& scratch, int num_sms,
+                        cudaStream_t stream);
+
+}  // namespace tsg

@@ -41,6 +41,9 @@
 // frees tensor memory and returns.
 #pragma once
 
+#include <type_traits>
+
+#include "ffn_epilogue.cuh"
 #include "ptx.cuh"
 
 namespace tsg {
@@ -101,6 +104,20 @@ struct GemmParams {
     int* status;          // plan status word
     uint64_t timeout_ns;
 };
+
+// What the kernel makes of the sums: the product itself, a linear layer's
+// output, or a gated layer's (whose B is [gate | up], and a tile of BN
+// columns of the product is BN / 2 of each and BN / 2 columns of C).
+enum EpiKind { kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2 };
+struct FfnParams : GemmParams {
+    FfnEpilogue epi;
+};
+template <int kEpi>
+using ParamsFor = std::conditional_t<kEpi == kEpiPlain, GemmParams, FfnParams>;
+
+// Columns of C in a tile of BN columns of the product.
+template <int BN, int kEpi>
+__host__ __device__ constexpr int c_cols() { return kEpi == kEpiGated ? BN / 2 : BN; }
 
 // One work unit: a whole tile, one of the S K-parts of a split tile, or a
 // stream-K segment of a tile.
@@ -236,17 +253,44 @@ __host__ __device__ constexpr uint32_t epi_smem_bytes() {
     return kEpiWarps * 2u * epi_buf_bytes<kOut>();  // 32 KiB (16-bit), none (fp32)
 }
 
-template <int kOut>
+template <int kOut, int kEpi = kEpiPlain>
 struct CStager {
     uint32_t buf0;   // this warp's first buffer; the second follows it
     uint32_t which;  // buffer to fill next
     int lane;
 
+    // The finished sums of this lane's row, columns [col0, col0 + 32): a
+    // linear layer's epilogue comes first.
+    __device__ __forceinline__ void put(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, int row0, int col0,
+                                        uint32_t (&r)[32]) {
+        if constexpr (kEpi == kEpiLinear)
+            linear_epilogue<kOut == kOutF32 ? kElemF32 : (kOut == kOutBF16 ? kElemBF16 : kElemF16)>(
+                p.epi, row0 + lane, p.M, col0, p.N, r);
+        store(p, tmC, row0, col0, r);
+    }
+
     // Convert 32 fp32 values (this lane's row, 32 consecutive columns) and
     // store the warp's 32 x 32 block at (row0, col0) of C.
-    __device__ __forceinline__ void put(const GemmParams& p, const CUtensorMap* tmC, int row0, int col0,
-                                        const uint32_t (&r)[32]) {
-        if constexpr (kOut == kOutF32) {
+    __device__ __forceinline__ void store(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, int row0, int col0,
+                                          const uint32_t (&r)[32]) {
+        if constexpr (kOut == kOutF32 && kEpi != kEpiPlain) {
+            // rows ldc apart, N of any size: vectors that start inside N but
+            // pass its end are stored one value at a time
+            const int row = row0 + lane;
+            if (row < p.M) {
+                float* dst = static_cast<float*>(p.C) + static_cast<int64_t>(row) * p.epi.ldc + col0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (col0 + 4 * j + 4 <= p.N) {
+                        st_global_v4(dst + 4 * j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (col0 + 4 * j + i < p.N) dst[4 * j + i] = __uint_as_float(r[4 * j + i]);
+                    }
+                }
+            }
+        } else if constexpr (kOut == kOutF32) {
             // straight to C: this lane's row, 8 16-byte vectors; N is a
             // multiple of 4, so a vector is wholly inside C or outside
             const int row = row0 + lane;
@@ -257,6 +301,20 @@ struct CStager {
                     if (col0 + 4 * j < p.N) st_global_v4(dst + 4 * j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
             }
         } else {
+            if constexpr (kEpi == kEpiLinear) {
+                // The copy engine writes whole 16-byte pieces of a row, past
+                // a row end inside one: the block that holds such an end is
+                // stored value by value.
+                if ((p.N & 7) != 0 && col0 + 32 > p.N) {
+                    if (row0 + lane < p.M) {
+                        const int64_t at = static_cast<int64_t>(row0 + lane) * p.epi.ldc + col0;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col0 + i < p.N) store16<kOut == kOutBF16>(p.C, at + i, __uint_as_float(r[i]));
+                    }
+                    return;
+                }
+            }
             const uint32_t buf = buf0 + which * epi_buf_bytes<kOut>();
             if (lane == 0) bulk_wait_group_read<1>();  // the store that used `buf` last has read it
             __syncwarp();
@@ -355,8 +413,8 @@ __device__ __forceinline__ void prefetch_sk_partials(const GemmParams& p, const 
                              kChunkBytes);
 }
 
-template <int BN, int kOut, class Release>
-__device__ __forceinline__ void drain_parts(const GemmParams& p, const CUtensorMap* tmC, CStager<kOut>& out,
+template <int BN, int kOut, int kEpi, class Release>
+__device__ __forceinline__ void drain_parts(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, CStager<kOut, kEpi>& out,
                                             const Unit& un, uint32_t tbase, int row0, int row_local, int64_t h,
                                             const EpiAux& aux, int c_begin, Release&& release) {
     const int n = un.nsplit, me = un.split;
@@ -441,23 +499,110 @@ __device__ __forceinline__ void drain_parts(const GemmParams& p, const CUtensorM
     }
 }
 
+// The gated layer's drain: 32 columns of H at a time, from the gate sums at
+// accumulator column c and the up sums at c + BN / 2, this warpgroup's
+// quarter [c_begin, c_begin + BN / 4) of each.  A unit that holds part of a
+// tile's K range counts the two chunks in together, on the gate chunk's
+// counter; otherwise the parts are added as drain_parts adds them.
 template <int BN, int kOut, class Release>
-__device__ __forceinline__ void drain_unit(const GemmParams& p, const CUtensorMap* tmC, CStager<kOut>& out,
+__device__ __forceinline__ void drain_gated(const FfnParams& p, const CUtensorMap* tmC,
+                                            CStager<kOut, kEpiGated>& out, const Unit& un, uint32_t tbase, int row0,
+                                            int row_local, int64_t h, const EpiAux& aux, int c_begin,
+                                            Release&& release) {
+    static_assert(BN % 128 == 0, "each warpgroup drains whole 32-column chunks of both halves");
+    const int n = un.nsplit, me = un.split;
+    const int q = row_local >> 5, lane = row_local & 31;
+    const int col0 = un.tn * (BN / 2);
+    constexpr int kNc = BN / 128;  // 32-column chunks of H in this warpgroup's part
+    const int first = n > 1 ? me * kNc / n : 0;
+#pragma unroll 1
+    for (int k = 0; k < kNc; ++k) {
+        int cl = first + k;
+        if (cl >= kNc) cl -= kNc;
+        const int c = c_begin + cl * 32;
+        const int gate = c >> 5, up = (c + BN / 2) >> 5;  // workspace chunks
+        uint32_t g[32], u[32];
+        tmem_ld_32x32b_x32(tbase + c, g);
+        tmem_ld_32x32b_x32(tbase + c + BN / 2, u);
+        tmem_ld_wait();
+        if (k == kNc - 1) release();  // this thread's accumulator part is in registers
+        if (n > 1) {
+            int* cnt = part_counter<BN>(p, h, gate, q);
+            int last = 0;
+            if (lane == 0) last = ld_acquire_gpu(cnt) == n - 1 ? 1 : 0;
+            last = __shfl_sync(0xffffffffu, last, 0);
+            if (!last) {
+                float* dg = part_chunk<BN>(p, un, aux, h, me, gate, q, lane);
+                float* du = part_chunk<BN>(p, un, aux, h, me, up, q, lane);
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    st_global_v4(dg + v * 128, g[4 * v], g[4 * v + 1], g[4 * v + 2], g[4 * v + 3]);
+                    st_global_v4(du + v * 128, u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
+                }
+                __threadfence();  // the partials are visible before they are counted
+                __syncwarp();
+                if (lane == 0) last = atom_acq_rel_gpu_add(cnt, 1) == n - 1 ? 1 : 0;
+                last = __shfl_sync(0xffffffffu, last, 0);
+                if (!last) continue;
+            }
+            __threadfence();  // the other parts' partials, counted in, are read after the count
+            // 0 + p_0 + ... + p_{n-1}, this part's own term at its place
+            auto sum = [&](int chunk, uint32_t (&r)[32]) {
+                float acc[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[j] = 0.0f;
+#pragma unroll 1
+                for (int s = 0; s < n; ++s) {
+                    if (s == me) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[j] = __fadd_rn(acc[j], __uint_as_float(r[j]));
+                        continue;
+                    }
+                    const float* src = part_chunk<BN>(p, un, aux, h, s, chunk, q, lane);
+                    float4 x[8];
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) x[v] = ld_global_cg_f4(src + v * 128);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        acc[4 * v] = __fadd_rn(acc[4 * v], x[v].x);
+                        acc[4 * v + 1] = __fadd_rn(acc[4 * v + 1], x[v].y);
+                        acc[4 * v + 2] = __fadd_rn(acc[4 * v + 2], x[v].z);
+                        acc[4 * v + 3] = __fadd_rn(acc[4 * v + 3], x[v].w);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(acc[j]);
+            };
+            sum(gate, g);
+            sum(up, u);
+            if (lane == 0) *reinterpret_cast<volatile int*>(cnt) = 0;  // ready for the next launch
+        }
+        gated_epilogue(p.epi, row0 + lane, p.M, col0 + c, p.N, g, u);
+        out.store(p, tmC, row0, col0 + c, g);
+    }
+}
+
+template <int BN, int kOut, int kEpi, class Release>
+__device__ __forceinline__ void drain_unit(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, CStager<kOut, kEpi>& out,
                                            const Unit& un, uint32_t tbase, int row0, int row_local, int64_t h,
                                            const EpiAux& aux, int c_begin, Release&& release) {
-    if (un.nsplit > 1) {
-        drain_parts<BN, kOut>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);
-        return;
-    }
-    const int col0 = un.tn * BN;
-    const int c_end = c_begin + BN / 2;  // this warpgroup's half of the columns
+    if constexpr (kEpi == kEpiGated) {
+        drain_gated<BN, kOut>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);
+    } else {
+        if (un.nsplit > 1) {
+            drain_parts<BN, kOut, kEpi>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);
+            return;
+        }
+        const int col0 = un.tn * BN;
+        const int c_end = c_begin + BN / 2;  // this warpgroup's half of the columns
 #pragma unroll 1
-    for (int c = c_begin; c < c_end; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tbase + c, r);
-        tmem_ld_wait();
-        if (c + 32 >= c_end) release();  // this thread's accumulator part is in registers
-        out.put(p, tmC, row0, col0 + c, r);
+        for (int c = c_begin; c < c_end; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tbase + c, r);
+            tmem_ld_wait();
+            if (c + 32 >= c_end) release();  // this thread's accumulator part is in registers
+            out.put(p, tmC, row0, col0 + c, r);
+        }
     }
 }
 
@@ -612,10 +757,10 @@ __device__ __forceinline__ bool drain_cs(const GemmParams& p, const CUtensorMap*
 // p.csplit), the CTAs of a cluster splitting each tile's K range and
 // chaining their partial sums through distributed shared memory
 // (drain_cs).
-template <int BN, int kOut, int kLayout, bool kF8 = false, bool kCS = false>
+template <int BN, int kOut, int kLayout, bool kF8 = false, bool kCS = false, int kEpi = kEpiPlain>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_sm103_1sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const GemmParams p) {
+                   const __grid_constant__ CUtensorMap tmC, const ParamsFor<kEpi> p) {
     using TS = TileShape<BN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -716,8 +861,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         const uint32_t a_dst = base + stage * TS::kStageBytes;
                         mbar_arrive_expect_tx(full_bar(stage), TS::kStageBytes);
-                        load_slice<kLayout, BN, false, kF8>(a_dst, a_dst + TS::kABytes, &tmA, &tmB, full_bar(stage), kb,
-                                                       un.tm * kBM, un.tn * BN);
+                        // (gated: BN / 2 gate columns, then as many up columns F further on)
+                        constexpr int kPiece = c_cols<BN, kEpi>();
+                        load_slice<kLayout, kPiece, false, kF8>(a_dst, a_dst + TS::kABytes, &tmA, &tmB,
+                                                                full_bar(stage), kb, un.tm * kBM, un.tn * kPiece);
+                        if constexpr (kEpi == kEpiGated)
+                            load_b<kLayout, kPiece, false, kF8>(a_dst + TS::kABytes + kPiece * kBK * 2, &tmB,
+                                                                full_bar(stage), kb, p.N + un.tn * kPiece);
                         outstanding |= 1u << stage;
                         out_parity = (out_parity & ~(1u << stage)) | (phase << stage);
                     }
@@ -777,10 +927,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // --------------------------------------------------- epilogue --
         const int q = warp & 3;              // TMEM lane quarter of this warp
         const int e = warp - 2;              // epilogue warp 0..7
-        const int c_begin = (e >> 2) * (BN / 2);  // warpgroup e/4 drains this half of the columns
+        // warpgroup e/4 drains this half of the tile's columns of C
+        const int c_begin = (e >> 2) * (c_cols<BN, kEpi>() / 2);
         const int etid = threadIdx.x - 64;   // 0..255
         const int row_local = q * 32 + lane;
-        CStager<kOut> out{epi_smem + static_cast<uint32_t>(e) * 2u * epi_buf_bytes<kOut>(), 0u, lane};
+        CStager<kOut, kEpi> out{epi_smem + static_cast<uint32_t>(e) * 2u * epi_buf_bytes<kOut>(), 0u, lane};
         int acc = 0;
         uint32_t acc_phase = 0;
         const EpiAux aux{static_cast<int64_t>(blockIdx.x), 1};
@@ -809,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         cs_bars + 8u * wg, cs_bars + 8u * (2 + wg), cs_phase, ctl, release))
                     break;
             } else {
-                drain_unit<BN, kOut>(p, &tmC, out, un, tbase, row0, row_local, un.slot, aux, c_begin, release);
+                drain_unit<BN, kOut, kEpi>(p, &tmC, out, un, tbase, row0, row_local, un.slot, aux, c_begin, release);
             }
             if (++acc == 2) {
                 acc = 0;

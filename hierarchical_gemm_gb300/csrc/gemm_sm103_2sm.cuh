@@ -51,10 +51,10 @@ __host__ __device__ constexpr uint32_t smem_bytes_2sm(int stages) {
     return 1024u + stages * PairShape<BN>::kStageBytes + epi_smem_bytes<kOut>() + 8u * (2 * stages + 5) + 16u;
 }
 
-template <int BN, int kOut, int kLayout, bool kF8 = false>
+template <int BN, int kOut, int kLayout, bool kF8 = false, int kEpi = kEpiPlain>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_sm103_2sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const GemmParams p) {
+                   const __grid_constant__ CUtensorMap tmC, const ParamsFor<kEpi> p) {
     using PS = PairShape<BN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -139,7 +139,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t a_dst = base + stage * PS::kStageBytes;
                         const int32_t arow = un.tm * (2 * kBM) + static_cast<int32_t>(half) * kBM;
                         // (wide tiles: this CTA's piece of each 256-column half)
-                        const int32_t bcol = un.tn * BN + static_cast<int32_t>(half) * PS::kPieceCols;
+                        // (gated: the tile's columns of B are as many gate columns, then
+                        // as many up columns F further on: the leader loads the gate half
+                        // and its peer the up half, or, wide, the first piece of each CTA
+                        // is gate columns and the second one up columns)
+                        constexpr bool kG = kEpi == kEpiGated;
+                        const int32_t step = kG && !PS::kWide ? p.N : static_cast<int32_t>(PS::kPieceCols);
+                        const int32_t bcol = un.tn * c_cols<BN, kEpi>() + static_cast<int32_t>(half) * step;
+                        [[maybe_unused]] const int32_t bcol2 = bcol + (kG ? p.N : 256);  // wide only
                         constexpr uint32_t kPieceBytes = PS::kPieceCols * kBK * 2;
                         if (leader) {
                             mbar_arrive_expect_tx(full_bar(stage), 2u * PS::kStageBytes);
@@ -147,14 +154,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                                             full_bar(stage), kb, arow, bcol);
                             if constexpr (PS::kWide)
                                 load_b<kLayout, PS::kPieceCols, false, kF8>(a_dst + PS::kABytes + kPieceBytes, &tmB,
-                                                                            full_bar(stage), kb, bcol + 256);
+                                                                            full_bar(stage), kb, bcol2);
                         } else {
                             const uint32_t fb = mapa_shared(full_bar(stage), 0u);
                             load_slice<kLayout, PS::kPieceCols, true, kF8>(a_dst, a_dst + PS::kABytes, &tmA, &tmB,
                                                                            fb, kb, arow, bcol);
                             if constexpr (PS::kWide)
                                 load_b<kLayout, PS::kPieceCols, true, kF8>(a_dst + PS::kABytes + kPieceBytes, &tmB,
-                                                                           fb, kb, bcol + 256);
+                                                                           fb, kb, bcol2);
                         }
                         outstanding |= 1u << stage;
                         out_parity = (out_parity & ~(1u << stage)) | (phase << stage);
@@ -229,10 +236,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ----------------------------------------------- epilogue (both) --
         const int q = warp & 3;                   // TMEM lane quarter of this warp
         const int e = warp - 2;                   // epilogue warp 0..7
-        const int c_begin = (e >> 2) * (BN / 2);  // warpgroup e/4 drains this half of the columns
+        // warpgroup e/4 drains this half of the tile's columns of C
+        const int c_begin = (e >> 2) * (c_cols<BN, kEpi>() / 2);
         const int etid = threadIdx.x - 64;
         const int row_local = q * 32 + lane;
-        CStager<kOut> out{epi_smem + static_cast<uint32_t>(e) * 2u * epi_buf_bytes<kOut>(), 0u, lane};
+        CStager<kOut, kEpi> out{epi_smem + static_cast<uint32_t>(e) * 2u * epi_buf_bytes<kOut>(), 0u, lane};
         int acc = 0;
         uint32_t acc_phase = 0;
         // Release accumulator `a` to the leader's MMA issuer.
@@ -264,9 +272,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t wh = un.slot * 2 + half;
             // (wide tiles: warpgroup e/4 drains accumulator e/4, the tile's
             // columns [256 (e/4), 256 (e/4) + 256), which are TMEM columns
-            // of the same numbers)
+            // of the same numbers; gated: every warp reads both accumulators,
+            // and the issuer waits for both releases)
             const int a_now = PS::kWide ? (e >> 2) : acc;
-            drain_unit<BN, kOut>(p, &tmC, out, un, tbase, row0, row_local, wh, aux, c_begin,
+            drain_unit<BN, kOut, kEpi>(p, &tmC, out, un, tbase, row0, row_local, wh, aux, c_begin,
                                  [&]() { release_acc(a_now); });
             if (PS::kWide) {
                 acc_phase ^= 1u;

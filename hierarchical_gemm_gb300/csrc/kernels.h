@@ -35,4 +35,20 @@ const void* kernel_1sm_f8(int block_n, int out_kind);
 const void* kernel_1sm_cs(int block_n, int out_kind);
 const void* kernel_2sm_f8(int block_n, int out_kind);
 
+// The kernels with a feed-forward epilogue (16-bit inputs; layouts RRR and
+// RCR, and CRR for a linear layer's weight gradient).  Linear: the tile
+// widths and outputs of the plain kernels, C of any width and stride.  Gated:
+// tiles of 128 and 256 columns of the product on one SM, 128, 256 and 512 on
+// a pair; 16-bit outputs.
+const void* kernel_linear_1sm_layout0(int block_n, int out_kind);
+const void* kernel_linear_1sm_layout1(int block_n, int out_kind);
+const void* kernel_linear_1sm_layout2(int block_n, int out_kind);
+const void* kernel_linear_2sm_layout0(int block_n, int out_kind);
+const void* kernel_linear_2sm_layout1(int block_n, int out_kind);
+const void* kernel_linear_2sm_layout2(int block_n, int out_kind);
+const void* kernel_gated_1sm_layout0(int block_n, int out_kind);
+const void* kernel_gated_1sm_layout1(int block_n, int out_kind);
+const void* kernel_gated_2sm_layout0(int block_n, int out_kind);
+const void* kernel_gated_2sm_layout1(int block_n, int out_kind);
+
 }  // namespace tsg

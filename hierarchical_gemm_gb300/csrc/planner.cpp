@@ -216,7 +216,7 @@ static tsgemm_status_t choose_cluster_split(int64_t M, int64_t N, int num_sms, c
 
 tsgemm_status_t choose_config(int64_t M, int64_t N, int64_t K, int dtype_in, int dtype_out,
                               int layout, int num_sms, const tsgemm_config_t* force,
-                              tsgemm_config_t* out) {
+                              tsgemm_config_t* out, unsigned widths) {
     if (!out) return TSGEMM_ERR_INVALID_ARG;
     tsgemm_status_t st = validate_problem(M, N, K, dtype_in, dtype_out, layout);
     if (st != TSGEMM_OK) return st;
@@ -271,6 +271,7 @@ tsgemm_status_t choose_config(int64_t M, int64_t N, int64_t K, int dtype_in, int
         if (bm == 256 && num_sms < 2) continue;
         for (int bn : bns) {
             if (bn == 512 && !wide) continue;
+            if (!(widths >> (bn / 64) & 1u)) continue;
             if (bm == 256 && bn != 128 && bn != 256 && bn != 512) continue;
             if (f.block_n && bn != f.block_n) continue;
             if (!f.block_n && bn > n_pad && bn != 64 && !(bm == 256 && bn == 128)) continue;

@@ -26,9 +26,12 @@ tsgemm_status_t validate_problem(int64_t M, int64_t N, int64_t K, int dtype_in, 
 
 // Fill *out with the configuration for the problem on a device with
 // `num_sms` SMs, honouring every non-zero field of `force` (may be null).
+// `widths`: the tile widths to choose from, bit w for 64 w columns.
+constexpr unsigned kAllWidths = ~0u;
+constexpr unsigned kGatedWidths = (1u << 2) | (1u << 4) | (1u << 8);  // 128, 256, 512
 tsgemm_status_t choose_config(int64_t M, int64_t N, int64_t K, int dtype_in, int dtype_out,
                               int layout, int num_sms, const tsgemm_config_t* force,
-                              tsgemm_config_t* out);
+                              tsgemm_config_t* out, unsigned widths = kAllWidths);
 
 // Dynamic shared memory per CTA of the kernel for this tile shape (block_m
 // 128: one SM per tile; 256: a CTA pair per tile), output type, ring depth

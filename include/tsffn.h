@@ -1,0 +1,188 @@
+/*
+ * tsffn.h -- C ABI of the feed-forward operators on GB300 (sm_103a): a
+ * linear layer with its epilogue, the gated feed-forward projection, their
+ * backward passes, and the clipping of gradients by their global norm.
+ *
+ * Operations.  X (M x K), W, C, ... are row-major with a row stride each (in
+ * elements).
+ *
+ *   linear    Z = X W + b,  C = act(Z) + R
+ *             W (K x N) stored K x N (TSGEMM_LAYOUT_RRR) or N x K (_RCR);
+ *             b (N) and R (M x N) may be absent.
+ *   backward  dZ = dC * act'(Z);  dX = dZ W^T;  dW = X^T dZ (stored as W is);
+ *             db = column sums of dZ.  (dR = dC.)
+ *   gated     G = X Wg, U = X Wu,  H = act(G) * U,  in one kernel
+ *             W = [Wg | Wu] stored K x 2F, or 2F x K with Wg's F rows first.
+ *   backward  dG = dH * U * act'(G), dU = dH * act(G);
+ *             dX = [dG dU] W^T;  dW = X^T [dG dU] (stored as W is).
+ *   clip      n = sqrt(sum of g^2 over every value of every tensor);
+ *             out = g * min(1, max_norm / (n + 1e-6)).
+ *
+ * Formats.  X, W, H and the gradients are all fp16 or all bf16; C and R are
+ * of that type or fp32; b and db of that type or fp32; dW of that type or
+ * fp32.  Clipped tensors are fp16, bf16 or fp32, mixed as the caller likes,
+ * each written in its own type.
+ *
+ * Numerics.  Products are exact and their sums fp32 (in the tensor cores, in
+ * an order fixed by the problem, or in a few-rows kernel's registers); bias,
+ * activation and residual are fp32 on those sums; each output is rounded
+ * once, to nearest, ties to even.  Saved pre-activations are fp32, so the
+ * backward pass starts from the sums the forward pass made.  dZ ([dG dU]) is
+ * rounded to the 16-bit type once, to be an operand of the tensor cores; db
+ * sums it before that rounding.  The squares of a clipped tensor are summed
+ * in fp32 over a few dozen values and in fp64 from there on, and squares
+ * that would leave fp32's range are formed in fp64.  Nothing depends on the
+ * order in which thread blocks run: results are reproducible run to run.
+ *
+ * Memory.  Device pointers of the current device, 16-byte aligned; row
+ * strides at least the row's length and multiples of 16 bytes.  Row lengths
+ * themselves are free, except that F must be a multiple of 8; nothing is
+ * written outside a matrix's own rows and columns.  An output must not overlap an input or another output; R may be C itself (same
+ * address and stride), and a clipped tensor its own input.
+ *
+ * Handles.  A tsffn_t holds the workspace of the calls made with it (split-K
+ * partials, column sums, a status word), allocated once.  Calls with one
+ * handle must be ordered on one stream; use one handle per stream.  Calls
+ * allocate nothing and may be captured into a CUDA graph; a graph's replays
+ * use the handle too, and must be ordered with its other calls.
+ *
+ * Errors, as in tsgemm.h: detected on the host before anything is launched,
+ * the arguments' own errors before the device is looked at
+ * (TSGEMM_ERR_INVALID_ARG for sizes < 1, missing or overlapping pointers,
+ * bad enums, memory that is not on the current device, a handle of another
+ * device; TSGEMM_ERR_ALIGNMENT; TSGEMM_ERR_UNSUPPORTED for a type or layout
+ * not listed above or sizes past 2^31 - 1).  Every device wait is bounded
+ * (1 s); one that expires sets the handle's status word, which
+ * tsffn_status() reads.
+ */
+#ifndef TSFFN_H
+#define TSFFN_H
+
+#include <stdint.h>
+
+#include "tsgemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct tsffn_s* tsffn_t;
+
+typedef enum {
+    TSFFN_ACT_NONE = 0,      /* z */
+    TSFFN_ACT_RELU = 1,      /* max(z, 0) */
+    TSFFN_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function */
+    TSFFN_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    TSFFN_ACT_SILU = 4,      /* z / (1 + exp(-z)) */
+    TSFFN_ACT_SIGMOID = 5    /* 1 / (1 + exp(-z)) */
+} tsffn_act_t;
+
+/* Make a handle on the current device (compute capability 10.3) and
+ * allocate its workspace.  On failure *out is NULL. */
+TSGEMM_API tsgemm_status_t tsffn_create(tsffn_t* out);
+
+/* Free the handle and its workspace; nothing that uses it may still be
+ * running.  NULL is accepted. */
+TSGEMM_API tsgemm_status_t tsffn_destroy(tsffn_t handle);
+
+/* The handle's status word: TSGEMM_OK, or TSGEMM_ERR_TIMEOUT when a bounded
+ * device wait of an earlier call expired.  Call after synchronising the
+ * stream; reading a timeout clears it and makes the handle usable again. */
+TSGEMM_API tsgemm_status_t tsffn_status(tsffn_t handle);
+
+/* Row stride, in floats, of the saved pre-activations of a linear layer of N
+ * columns (a gated layer of F: pass 2 F). */
+#define TSFFN_SAVED_LD(n) (((int64_t)(n) + 7) / 8 * 8)
+
+typedef struct {
+    int64_t M, N, K;
+    int32_t dtype;      /* X, W: TSGEMM_F16 or TSGEMM_BF16 */
+    int32_t dtype_out;  /* C, R: dtype or TSGEMM_F32 */
+    int32_t dtype_bias; /* bias: dtype or TSGEMM_F32 */
+    int32_t layout;     /* TSGEMM_LAYOUT_RRR or TSGEMM_LAYOUT_RCR */
+    int32_t act;        /* tsffn_act_t */
+    int32_t reserved;   /* 0 */
+    const void* X;
+    const void* W;
+    const void* bias;     /* N values, or NULL */
+    const void* residual; /* M x N, or NULL */
+    void* C;
+    float* saved;         /* M x TSFFN_SAVED_LD(N) floats that receive Z, or NULL */
+    int64_t ldx, ldw, ldr, ldc;
+} tsffn_linear_args;
+
+/* Enqueue a linear layer on `stream` (a cudaStream_t). */
+TSGEMM_API tsgemm_status_t tsffn_linear(tsffn_t handle, const tsffn_linear_args* args, void* stream);
+
+typedef struct {
+    int64_t M, N, K;
+    int32_t dtype;      /* dC, X, W, dX */
+    int32_t dtype_dw;   /* dW: dtype or TSGEMM_F32 */
+    int32_t dtype_bias; /* dbias: dtype or TSGEMM_F32 */
+    int32_t layout;
+    int32_t act;
+    int32_t reserved;   /* 0 */
+    const void* dC;
+    const void* X;      /* may be NULL without dW */
+    const void* W;      /* may be NULL without dX */
+    const float* saved; /* what tsffn_linear saved; unused without an activation */
+    void* dX;           /* each of the three outputs may be NULL */
+    void* dW;
+    void* dbias;
+    void* workspace;    /* M * TSFFN_SAVED_LD(N) 16-bit values; unused without an activation */
+    int64_t lddc, ldx, ldw, lddx, lddw;
+} tsffn_linear_backward_args;
+
+TSGEMM_API tsgemm_status_t tsffn_linear_backward(tsffn_t handle, const tsffn_linear_backward_args* args,
+                                                 void* stream);
+
+typedef struct {
+    int64_t M, F, K;
+    int32_t dtype;
+    int32_t layout;
+    int32_t act;
+    int32_t reserved; /* 0 */
+    const void* X;
+    const void* W;
+    void* H;
+    float* saved;     /* M x 2 F floats that receive [G U], or NULL */
+    int64_t ldx, ldw, ldh;
+} tsffn_gated_args;
+
+/* Enqueue a gated projection on `stream`. */
+TSGEMM_API tsgemm_status_t tsffn_gated(tsffn_t handle, const tsffn_gated_args* args, void* stream);
+
+typedef struct {
+    int64_t M, F, K;
+    int32_t dtype;
+    int32_t dtype_dw;
+    int32_t layout;
+    int32_t act;
+    const void* dH;
+    const void* X;      /* may be NULL without dW */
+    const void* W;      /* may be NULL without dX */
+    const float* saved; /* what tsffn_gated saved */
+    void* dX;           /* either output may be NULL */
+    void* dW;
+    void* workspace;    /* M * 2 F 16-bit values */
+    int64_t lddh, ldx, ldw, lddx, lddw;
+} tsffn_gated_backward_args;
+
+TSGEMM_API tsgemm_status_t tsffn_gated_backward(tsffn_t handle, const tsffn_gated_backward_args* args,
+                                                void* stream);
+
+/* Clip `count` dense tensors (count >= 0) of numel[i] >= 0 values of
+ * dtype[i] by their global norm: out[i] (which may be grads[i]) receives
+ * grads[i] * min(1, max_norm / (norm + 1e-6)), *norm (a device float) the
+ * norm.  A norm that is not finite takes its course through that formula.
+ * Tensors need only be aligned to their own type; 16-byte aligned ones are
+ * read in 16-byte vectors.  max_norm >= 0 (infinity: the norm alone). */
+TSGEMM_API tsgemm_status_t tsffn_clip_grad_norm(tsffn_t handle, int64_t count, const void* const* grads,
+                                                void* const* out, const int64_t* numel, const int32_t* dtype,
+                                                float max_norm, float* norm, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TSFFN_H */
