@@ -193,6 +193,25 @@ struct Product {
 };
 
 tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
+    if (g.kind != tsg::kEpiPlain && g.layout != TSGEMM_LAYOUT_CRR && g.M <= tsg::kFewRows) {
+        tsg::FewRowsArgs a{};
+        a.M = g.M;
+        a.N = g.kind == tsg::kEpiGated ? g.N / 2 : g.N;
+        a.K = g.K;
+        a.X = g.A;
+        a.W = g.B;
+        a.C = g.C;
+        a.ldx = g.lda;
+        a.ldw = g.ldb;
+        a.epi = g.epi;
+        a.out_f32 = g.dout == TSGEMM_F32;
+        if (tsg::launch_few_rows(a, g.din == TSGEMM_BF16, g.layout == TSGEMM_LAYOUT_RCR, g.kind == tsg::kEpiGated,
+                                 h->num_sms, stream) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return TSGEMM_ERR_CUDA;
+        }
+        return TSGEMM_OK;
+    }
     FfnConfig f;
     const tsgemm_status_t st = make_config(h, g.kind, g.M, g.N, g.K, g.din, g.dout, g.layout, &f);
     if (st != TSGEMM_OK) return st;
@@ -398,12 +417,13 @@ Mat weights(const void* W, int layout, int64_t N, int64_t K, int64_t ldw, int64_
 
 // A product without an epilogue, into C of any width and stride: the plain
 // kernels where they can store it (rows of whole 16-byte pieces, fp32 rows
-// dense), else the linear layer's with nothing to do.
+// dense), else the linear layer's with nothing to do, which also covers few
+// rows.
 Product plain_product(int64_t M, int64_t N, int64_t K, int din, int dout, int layout, const void* A, int64_t lda,
                       const void* B, int64_t ldb, void* C, int64_t ldc) {
     FfnEpilogue e{};
     e.ldc = ldc;
-    const bool plain = dout == TSGEMM_F32 ? ldc == N : N % 8 == 0;
+    const bool plain = M > tsg::kFewRows && (dout == TSGEMM_F32 ? ldc == N && N % 4 == 0 : N % 8 == 0);
     return Product{plain ? tsg::kEpiPlain : tsg::kEpiLinear, M, N, K, din, dout, layout, A, B, C, lda, ldb, ldc, e};
 }
 
@@ -441,6 +461,10 @@ tsgemm_status_t allocate(tsffn_s* h) {
         cudaMalloc(&h->clip_partials, (kClipPartials + 1) * sizeof(double)) != cudaSuccess) {
         (void)cudaGetLastError();
         return TSGEMM_ERR_OOM;
+    }
+    if (tsg::init_few_rows() != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSGEMM_ERR_CUDA;
     }
     cudaStream_t s = nullptr;
     bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;

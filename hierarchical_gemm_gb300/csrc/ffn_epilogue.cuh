@@ -13,6 +13,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "ffn_kernels.h"
 #include "ptx.cuh"
 
 namespace tsg {
@@ -152,9 +153,7 @@ __device__ __forceinline__ void load8_f32(const float* p, int64_t i, int64_t n, 
         for (int j = 0; j < 8; ++j) v[j] = i + j < n ? p[i + j] : 0.0f;
     }
 }
-// The same for a vector whose type (ElemKind) is known only when the kernel
-// runs.
-enum ElemKind { kElemNone = 0, kElemF16 = 1, kElemBF16 = 2, kElemF32 = 3 };
+// The same for a vector whose type is known only when the kernel runs.
 __device__ __forceinline__ void load8(int kind, const void* p, int64_t i, int64_t n, float (&v)[8]) {
     if (kind == kElemBF16)
         load8_16<true>(p, i, n, v);
@@ -165,19 +164,6 @@ __device__ __forceinline__ void load8(int kind, const void* p, int64_t i, int64_
 }
 
 // --------------------------------------------------------- the epilogue --
-
-// What an epilogue kernel does beyond C = A B.  Columns are those of the
-// product for a linear layer (p.N of them), those of H for the gated one.
-struct FfnEpilogue {
-    const void* bias;      // N values (bias_kind), or none
-    const void* residual;  // M x N of the output type, rows ldr apart, or null
-    float* saved;          // fp32 pre-activations, rows lds apart (linear: N
-                           // columns; gated: F gate columns, then F up ones), or null
-    int64_t ldr, lds, ldc; // in elements (ldc: for what is not stored through
-                           // the tensor map of C)
-    int32_t bias_kind;     // ElemKind
-    int32_t act;           // ActKind
-};
 
 // Lane's row `row`, columns [col, col + 32) of the fp32 sums in r: writes
 // them to the saved pre-activations at column `at` (the linear layer's own

@@ -9,6 +9,40 @@
 
 namespace tsg {
 
+// Types of a vector that a kernel learns when it runs.
+enum ElemKind { kElemNone = 0, kElemF16 = 1, kElemBF16 = 2, kElemF32 = 3 };
+
+// What an epilogue kernel does beyond C = A B.  Columns are those of the
+// product for a linear layer (p.N of them), those of H for the gated one.
+struct FfnEpilogue {
+    const void* bias;      // N values (bias_kind), or none
+    const void* residual;  // M x N of the output type, rows ldr apart, or null
+    float* saved;          // fp32 pre-activations, rows lds apart (linear: N
+                           // columns; gated: F gate columns, then F up ones), or null
+    int64_t ldr, lds, ldc; // in elements (ldc: for what is not stored through
+                           // the tensor map of C)
+    int32_t bias_kind;     // ElemKind
+    int32_t act;           // ActKind
+};
+
+// The linear and gated layers for M <= kFewRows rows of X.  N: columns of
+// the output (gated: F).
+constexpr int64_t kFewRows = 16;
+struct FewRowsArgs {
+    int64_t M, N, K;
+    const void* X;
+    const void* W;
+    void* C;
+    int64_t ldx, ldw;
+    FfnEpilogue epi;
+    int32_t out_f32;
+    int32_t kparts;  // blocks of a cluster that split K (set by the launch)
+};
+// Once per device, before the first launch there.
+cudaError_t init_few_rows();
+cudaError_t launch_few_rows(const FewRowsArgs& args, bool bf16, bool rcr, bool gated, int num_sms,
+                            cudaStream_t stream);
+
 // Column sums that several CTAs make together: fp32 partials
 // [row chunk][columns], and one arrival counter per strip of columns (zero
 // between launches).
