@@ -83,7 +83,7 @@ struct tsffn_s {
     int num_sms;
     float* ws;
     int* counters;
-    int* clip_counter;
+    int* clip_counters;
     double* clip_partials;
     float* clip_coef;
     int* status;
@@ -193,10 +193,13 @@ struct Product {
 };
 
 tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
-    if (g.kind != tsg::kEpiPlain && g.layout != TSGEMM_LAYOUT_CRR && g.M <= tsg::kFewRows) {
+    const bool is_gated = g.kind == tsg::kEpiGated;
+    const int64_t columns = is_gated ? g.N / 2 : g.N;
+    if (g.kind != tsg::kEpiPlain && g.layout != TSGEMM_LAYOUT_CRR &&
+        tsg::few_rows_fit(g.M, columns, g.K, g.layout == TSGEMM_LAYOUT_RCR, is_gated, h->num_sms)) {
         tsg::FewRowsArgs a{};
         a.M = g.M;
-        a.N = g.kind == tsg::kEpiGated ? g.N / 2 : g.N;
+        a.N = columns;
         a.K = g.K;
         a.X = g.A;
         a.W = g.B;
@@ -205,8 +208,8 @@ tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
         a.ldw = g.ldb;
         a.epi = g.epi;
         a.out_f32 = g.dout == TSGEMM_F32;
-        if (tsg::launch_few_rows(a, g.din == TSGEMM_BF16, g.layout == TSGEMM_LAYOUT_RCR, g.kind == tsg::kEpiGated,
-                                 h->num_sms, stream) != cudaSuccess) {
+        if (tsg::launch_few_rows(a, g.din == TSGEMM_BF16, g.layout == TSGEMM_LAYOUT_RCR, is_gated, h->num_sms,
+                                 stream) != cudaSuccess) {
             (void)cudaGetLastError();
             return TSGEMM_ERR_CUDA;
         }
@@ -218,8 +221,8 @@ tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return TSGEMM_ERR_CUDA;
     const tsgemm_config_t& c = f.cfg;
-    const bool pair = c.block_m == 256, gated = g.kind == tsg::kEpiGated;
-    const int64_t n_out = gated ? g.N / 2 : g.N;       // columns of C
+    const bool pair = c.block_m == 256, gated = is_gated;
+    const int64_t n_out = columns;
     const int64_t tile_out = gated ? c.block_n / 2 : c.block_n;
 
     alignas(64) CUtensorMap tmA, tmB, tmC;
@@ -423,7 +426,8 @@ Product plain_product(int64_t M, int64_t N, int64_t K, int din, int dout, int la
                       const void* B, int64_t ldb, void* C, int64_t ldc) {
     FfnEpilogue e{};
     e.ldc = ldc;
-    const bool plain = M > tsg::kFewRows && (dout == TSGEMM_F32 ? ldc == N && N % 4 == 0 : N % 8 == 0);
+    const bool few = layout != TSGEMM_LAYOUT_CRR && M <= tsg::kFewRows;
+    const bool plain = !few && (dout == TSGEMM_F32 ? ldc == N && N % 4 == 0 : N % 8 == 0);
     return Product{plain ? tsg::kEpiPlain : tsg::kEpiLinear, M, N, K, din, dout, layout, A, B, C, lda, ldb, ldc, e};
 }
 
@@ -452,8 +456,8 @@ tsgemm_status_t cuda_status(cudaError_t e) {
     return TSGEMM_ERR_CUDA;
 }
 
-// counters | clip counter | status word
-constexpr size_t kWords = static_cast<size_t>(kCounters) + 2;
+// counters | the clipping's two | status word
+constexpr size_t kWords = static_cast<size_t>(kCounters) + 3;
 
 tsgemm_status_t allocate(tsffn_s* h) {
     if (cudaMalloc(&h->ws, static_cast<size_t>(kWorkspaceBytes)) != cudaSuccess ||
@@ -475,8 +479,8 @@ tsgemm_status_t allocate(tsffn_s* h) {
         (void)cudaGetLastError();
         return TSGEMM_ERR_CUDA;
     }
-    h->clip_counter = h->counters + kCounters;
-    h->status = h->counters + kCounters + 1;
+    h->clip_counters = h->counters + kCounters;
+    h->status = h->counters + kCounters + 2;
     h->clip_coef = reinterpret_cast<float*>(h->clip_partials + kClipPartials);
     return TSGEMM_OK;
 }
@@ -742,7 +746,8 @@ tsgemm_status_t tsffn_clip_grad_norm(tsffn_t h, int64_t count, const void* const
             if (st == TSGEMM_OK && out[i] != grads[i]) st = check_device_ptr(out[i], h->device);
         }
         if (st != TSGEMM_OK) return st;
-        const tsg::ClipScratch scratch{h->clip_partials, kClipPartials, h->clip_counter, h->clip_coef};
+        const tsg::ClipScratch scratch{h->clip_partials, kClipPartials, h->clip_counters, h->clip_coef, h->status,
+                                       kTimeoutNs};
         return cuda_status(tsg::launch_clip(count, grads, out, numel, dtype, max_norm, norm, scratch, h->num_sms,
                                             static_cast<cudaStream_t>(stream)));
     });

@@ -25,9 +25,23 @@ struct FfnEpilogue {
     int32_t act;           // ActKind
 };
 
-// The linear and gated layers for M <= kFewRows rows of X.  N: columns of
-// the output (gated: F).
-constexpr int64_t kFewRows = 16;
+// The linear and gated layers for a few rows of X.  N: columns of the output
+// (gated: F).
+//
+// Whether they are the faster way, against the 128-row tiles (us a call,
+// bf16, N x K):
+//   W stored N x K   4096 x 4096   28672 x 4096   8192 x 8192   8192 x 14336
+//     1 row          8.0 / 17.8    37.5 / 58.1    24.8 / -      41.0 / 62.1
+//     16 rows        9.2 / 17.4    42.3 / 44.7    27.9 / -      45.2 / 52.0
+//     32 rows        12.0 / 17.6   51.1 / 44.7    33.8 / 35.3   54.3 / 51.4
+//   stored K x N
+//     8 rows         9.1 / 17.6    45 / 54        26.8 / -      40.4 / 49.2
+//     16 rows        10.5 / 17.5   51 / 42        28.3 / -      42.5 / 48.9
+//     32 rows        13.4 / 17.4   -              32.9 / 33.3   49.4 / 49.3
+// so: up to 8 rows always; to 32 rows up to 2^26 weights (to 16: any); W
+// stored K x N no more strips than SMs.
+constexpr int64_t kFewRows = 32;
+bool few_rows_fit(int64_t M, int64_t N, int64_t K, bool rcr, bool gated, int num_sms);
 struct FewRowsArgs {
     int64_t M, N, K;
     const void* X;
@@ -82,13 +96,16 @@ struct GatedGradArgs {
 };
 cudaError_t launch_gated_grad(const GatedGradArgs& a, int num_sms, cudaStream_t stream);
 
-// Scratch of the global norm: one fp64 partial per thread block, a counter
-// (zero between launches) and the coefficient the scaling pass reads.
+// Scratch of the global norm: one fp64 sum per thread block, two counters
+// (zero between launches), the coefficient a scaling launch reads, and the
+// status word of a wait that ran out.
 struct ClipScratch {
     double* partials;
     int64_t max_partials;
-    int* counter;
+    int* counters;
     float* coef;
+    int* status;
+    uint64_t timeout_ns;
 };
 cudaError_t launch_clip(int64_t count, const void* const* grads, void* const* out, const int64_t* numel,
                         const int32_t* dtype, float max_norm, float* norm, const ClipScratch& scratch, int num_sms,

@@ -1,6 +1,6 @@
 // ffn_rows.cu -- the linear and gated layers for a few rows of X (decoding:
 // one token of each of a few sequences), where the weights' bytes are the
-// work: every weight is read once and meets at most 16 rows.
+// work: every weight is read once and meets at most 32 rows.
 //
 // A thread block owns strips of output columns; its 8 warps split K, hold
 // fp32 sums in registers (tensor-core fragments: mma.sync m16n8k16 with 16
@@ -12,9 +12,9 @@
 // in a fixed order.
 //
 // HBM bounds it, so what counts is bytes in flight: one block an SM, and
-// each thread keeps a ring of 16-byte asynchronous copies of the weights it
-// will use itself (no barrier guards a slot) that runs ahead across strips,
-// over 100 KiB an SM in all.  The copies take a length, so the last partial
+// each warp keeps a ring of 16-byte asynchronous copies of its own (no
+// block-wide barrier guards a slot) that runs ahead across strips, over
+// 100 KiB an SM in all.  The copies take a length, so the last partial
 // vectors of K and of the columns read as zeros past their end.
 //
 // The order of k within a fragment is free as long as W and X agree, so a
@@ -84,7 +84,12 @@ struct RowsShape {
     static constexpr int kFrags = kRCR ? 1 : 4;    // 16-column fragments of a group
     static constexpr int kWVecs = kRCR ? 4 : 8;    // 16-byte vectors of W that a thread takes in a step
     static constexpr int kVecs = kWVecs + MT;      // and of X
-    static constexpr int kDepth = kRCR ? 8 : 4;    // steps in flight
+    // Blocks an SM, and steps in flight of each, as many as shared memory
+    // holds.  W stored N x K with more than 8 rows of X has two shallower
+    // blocks, whose arithmetic overlaps (8192 x 8192: 16 rows 28.8 -> 27.9 us,
+    // 32 rows 38.4 -> 33.8); the other forms are faster with one.
+    static constexpr int kPerSM = kRCR && MT > 1 ? 2 : 1;
+    static constexpr int kDepth = kRCR ? (MT == 1 ? 8 : (MT == 2 ? 4 : 3)) : (MT > 2 ? 3 : 4);
     static constexpr int kLd = kStrip + 4;         // row of sums (m) in shared memory, padded against conflicts
     static constexpr uint32_t kStepBytes = kVecs * 32 * 16;  // of a warp's ring
     static constexpr uint32_t kRingBytes = kWarps * kDepth * kStepBytes;
@@ -95,7 +100,7 @@ struct RowsShape {
 // groups of columns: neighbours, or for the gated layer the same columns of
 // the gate and of the up half.
 template <bool kBF16, bool kRCR, bool kGated, int MT>
-__global__ void __launch_bounds__(32 * kWarps, 1) few_rows_sm103(const FewRowsArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, (RowsShape<kRCR, MT>::kPerSM)) few_rows_sm103(const FewRowsArgs a) {
     using S = RowsShape<kRCR, MT>;
     constexpr int kGroup = S::kGroup, kStrip = S::kStrip, kFrags = S::kFrags, kLd = S::kLd, kDepth = S::kDepth;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -121,49 +126,84 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_rows_sm103(const FewRowsAr
     // kWarps-th.
     const int64_t blocks = (a.K + S::kStepK - 1) / S::kStepK;
     const int64_t k0 = blocks * rank / parts + warp, k1 = blocks * (rank + 1) / parts;
-    const uint32_t ring = smem_u32(smem_raw) + static_cast<uint32_t>(warp) * (kDepth * S::kStepBytes) + lane * 16u;
+    //
+    // Who copies what: W stored N x K, each thread its own vectors.  Stored
+    // K x N, 8 neighbouring threads copy 128 bytes of a row (thread (g, t)
+    // copying its own would touch 4 rows at a time in 16-byte pieces, and
+    // ask L2 for every 32-byte sector twice), so thread l copies the vectors
+    // of thread (gl, tl) = (l mod 8, l / 8); both sides address a vector by
+    // (g, t) in an order free of bank conflicts.
+    const uint32_t warp_ring = smem_u32(smem_raw) + static_cast<uint32_t>(warp) * (kDepth * S::kStepBytes);
+    auto place = [](int vg, int vt) { return static_cast<uint32_t>(vt * 8 + (vg ^ (2 * vt))) * 16u; };
+    const int gl = lane & 7, tl = lane >> 3;
+    const uint32_t ring_wr = warp_ring + (kRCR ? lane * 16u : place(gl, tl));
+    const uint32_t ring_rd = warp_ring + (kRCR ? lane * 16u : place(g, t));
+    // (X for W stored K x N: 16-byte vectors of 8 k, two a row)
+    const uint32_t ring_rdx = warp_ring + (kRCR ? lane * 16u : place(g, t >> 1));
 
     // The copies of one step: of the cursor's strip and block, which moves on.
+    // Addresses are kept and moved along (pw: this thread's first vector of W
+    // in the step; its others lie `vec_off` further on), and what may be read
+    // of each is worked out once a strip; the last, partial block of K looks
+    // at every vector again.
+    const int vg = kRCR ? g : gl, vt = kRCR ? t : tl;         // the vectors' place in a step
+    const int64_t vec_k = kRCR ? 8 * vt : 4 * vt;             // first k of them, of the step
+    const int64_t step_elems = kRCR ? S::kStepK * kWarps : S::kStepK * kWarps * a.ldw;
+    const int64_t group_off = kRCR ? (kGated ? a.N : kGroup) * a.ldw : (kGated ? a.N : kGroup);
+    auto vec_off = [&](int v) {
+        return kRCR ? (v >> 1) * group_off + (v & 1) * 8 * a.ldw : (v >> 2) * group_off + (v & 3) * a.ldw;
+    };
+    constexpr int kColSets = kRCR ? 4 : 2;  // vectors of W that can differ in their columns
     int64_t cs = k0 < k1 ? strip0 : strips, cb = k0;
+    const uint16_t* pw = W;
+    const uint16_t* px = X;
+    int wbytes[kColSets];
+    auto enter_strip = [&] {
+        if (cs >= strips) return;
+        if constexpr (kRCR) {
+            pw = W + (col0(cs, 0) + vg) * a.ldw + cb * S::kStepK + vec_k;
+            px = X + vg * a.ldx + cb * S::kStepK + vec_k;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) wbytes[v] = col0(cs, v >> 1) + vg + 8 * (v & 1) < col1(v >> 1) ? 16 : 0;
+        } else {
+            pw = W + (cb * S::kStepK + vec_k) * a.ldw + col0(cs, 0) + 8 * vg;
+            px = X + vg * a.ldx + cb * S::kStepK + 8 * vt;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) wbytes[j] = bytes_in(col0(cs, j) + 8 * vg, col1(j));
+        }
+    };
+    enter_strip();
     auto issue = [&](uint32_t slot) {
         if (cs < strips) {
-            const uint32_t dst = ring + slot * S::kStepBytes;
-            const int64_t k = cb * S::kStepK;
-            if constexpr (kRCR) {
-                // columns g and g + 8 of each group, 8 k
-                const int bytes = bytes_in(k + t * 8, a.K);
+            const uint32_t dst = ring_wr + slot * S::kStepBytes;
+            const bool whole = (cb + 1) * S::kStepK <= a.K;
+            const int64_t k = cb * S::kStepK + vec_k;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int64_t n = col0(cs, v >> 1) + g + 8 * (v & 1);
-                    const bool in = n < col1(v >> 1) && bytes > 0;
-                    cp_async16(dst + v * 512u, in ? W + n * a.ldw + k + t * 8 : W, in ? bytes : 0);
+            for (int v = 0; v < S::kWVecs; ++v) {
+                int bytes = wbytes[kRCR ? v : v >> 2];
+                if (!whole) {
+                    if constexpr (kRCR)
+                        bytes = bytes ? bytes_in(k, a.K) : 0;
+                    else
+                        bytes = k + (v & 3) < a.K ? bytes : 0;
                 }
+                cp_async16(dst + v * 512u, bytes ? pw + vec_off(v) : W, bytes);
+            }
+            if (kRCR || vt < 2) {  // (W stored K x N: a row of X has two vectors in a step)
+                const int xbytes = whole ? 16 : bytes_in(cb * S::kStepK + 8 * vt, a.K);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    const bool in = g + 8 * i < a.M && bytes > 0;
-                    cp_async16(dst + (4 + i) * 512u, in ? X + (g + 8 * i) * a.ldx + k + t * 8 : X, in ? bytes : 0);
-                }
-            } else {
-                // columns 8 g .. + 7 of each group at k + 4 t .. + 3
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    const int64_t n = col0(cs, v >> 2) + 8 * g, row = k + 4 * t + (v & 3);
-                    const int bytes = row < a.K ? bytes_in(n, col1(v >> 2)) : 0;
-                    cp_async16(dst + v * 512u, bytes ? W + row * a.ldw + n : W, bytes);
-                }
-                // (8 bytes of X are needed: the 8 values from 4 t - 4 (t % 2) on hold them)
-                const int64_t kx = k + 8 * (t >> 1);
-                const int bytes = bytes_in(kx, a.K);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const bool in = g + 8 * i < a.M && bytes > 0;
-                    cp_async16(dst + (8 + i) * 512u, in ? X + (g + 8 * i) * a.ldx + kx : X, in ? bytes : 0);
+                    const int bytes = vg + 8 * i < a.M ? xbytes : 0;
+                    cp_async16(dst + (S::kWVecs + i) * 512u, bytes ? px + 8 * i * a.ldx : X, bytes);
                 }
             }
             cb += kWarps;
+            pw += step_elems;
+            px += S::kStepK * kWarps;
             if (cb >= k1) {
                 cb = k0;
                 cs += strip_step;
+                enter_strip();
             }
         }
         cp_async_commit();  // (an empty group past the end keeps the count)
@@ -176,12 +216,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_rows_sm103(const FewRowsAr
         float d[2][kFrags][MT][4] = {};
         for (int64_t b = k0; b < k1; b += kWarps) {
             cp_async_wait<kDepth - 1>();  // this thread's oldest step has landed
-            const uint32_t src = ring + slot * S::kStepBytes;
+            if constexpr (!kRCR) __syncwarp();  // and so have the other threads'
+            const uint32_t src = ring_rd + slot * S::kStepBytes, srcx = ring_rdx + slot * S::kStepBytes;
             uint4 w[S::kWVecs], x[MT];
 #pragma unroll
             for (int v = 0; v < S::kWVecs; ++v) w[v] = ld_shared_u4(src + v * 512u);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) x[i] = ld_shared_u4(src + (S::kWVecs + i) * 512u);
+            for (int i = 0; i < MT; ++i) x[i] = ld_shared_u4(srcx + (S::kWVecs + i) * 512u);
             if constexpr (kRCR) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -210,7 +251,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_rows_sm103(const FewRowsAr
                     frag(j, 3, w[4 * j].w, w[4 * j + 1].w, w[4 * j + 2].w, w[4 * j + 3].w);
                 }
             }
-            issue(slot);  // the slot's vectors are in registers
+            if constexpr (!kRCR) __syncwarp();  // every thread has its vectors in registers
+            issue(slot);
             slot = slot + 1 == kDepth ? 0 : slot + 1;
         }
 
@@ -293,38 +335,34 @@ __global__ void __launch_bounds__(32 * kWarps, 1) few_rows_sm103(const FewRowsAr
 struct RowsKernel {
     const void* kernel;
     uint32_t smem;
+    int per_sm;
 };
-// By (bf16, W stored N x K, gated, more than 8 rows).
 template <bool kBF16, bool kRCR, bool kGated, int MT>
 RowsKernel entry() {
-    return {reinterpret_cast<const void*>(&few_rows_sm103<kBF16, kRCR, kGated, MT>), RowsShape<kRCR, MT>::kSmemBytes};
+    using S = RowsShape<kRCR, MT>;
+    static_assert(S::kPerSM * (S::kSmemBytes + 1024) <= 233472, "shared memory of an SM");
+    return {reinterpret_cast<const void*>(&few_rows_sm103<kBF16, kRCR, kGated, MT>), S::kSmemBytes, S::kPerSM};
 }
-RowsKernel rows_kernel(int i) {
-    switch (i) {
-        case 0: return entry<false, false, false, 1>();
-        case 1: return entry<false, false, false, 2>();
-        case 2: return entry<false, false, true, 1>();
-        case 3: return entry<false, false, true, 2>();
-        case 4: return entry<false, true, false, 1>();
-        case 5: return entry<false, true, false, 2>();
-        case 6: return entry<false, true, true, 1>();
-        case 7: return entry<false, true, true, 2>();
-        case 8: return entry<true, false, false, 1>();
-        case 9: return entry<true, false, false, 2>();
-        case 10: return entry<true, false, true, 1>();
-        case 11: return entry<true, false, true, 2>();
-        case 12: return entry<true, true, false, 1>();
-        case 13: return entry<true, true, false, 2>();
-        case 14: return entry<true, true, true, 1>();
-        default: return entry<true, true, true, 2>();
+template <bool kBF16, bool kRCR, bool kGated>
+RowsKernel by_rows(int groups) {
+    return groups == 1 ? entry<kBF16, kRCR, kGated, 1>()
+                       : (groups == 2 ? entry<kBF16, kRCR, kGated, 2>() : entry<kBF16, kRCR, kGated, 4>());
+}
+// groups of 8 rows: 1, 2 or 4
+RowsKernel rows_kernel(bool bf16, bool rcr, bool gated, int groups) {
+    if (bf16) {
+        if (rcr) return gated ? by_rows<true, true, true>(groups) : by_rows<true, true, false>(groups);
+        return gated ? by_rows<true, false, true>(groups) : by_rows<true, false, false>(groups);
     }
+    if (rcr) return gated ? by_rows<false, true, true>(groups) : by_rows<false, true, false>(groups);
+    return gated ? by_rows<false, false, true>(groups) : by_rows<false, false, false>(groups);
 }
 
 }  // namespace
 
 cudaError_t init_few_rows() {
-    for (int i = 0; i < 16; ++i) {
-        const RowsKernel k = rows_kernel(i);
+    for (int i = 0; i < 24; ++i) {
+        const RowsKernel k = rows_kernel(i & 1, i & 2, i & 4, 1 << (i >> 3));
         const cudaError_t st =
             cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
         if (st != cudaSuccess) return st;
@@ -332,19 +370,33 @@ cudaError_t init_few_rows() {
     return cudaSuccess;
 }
 
+bool few_rows_fit(int64_t M, int64_t N, int64_t K, bool rcr, bool gated, int num_sms) {
+    if (M <= 8) return true;
+    if (M > kFewRows) return false;
+    if (M > 16 && (gated ? 2 * N : N) * K > (int64_t{1} << 26)) return false;
+    const int64_t cols = gated ? 64 : 128;
+    return rcr || (N + cols - 1) / cols <= num_sms;
+}
+
 cudaError_t launch_few_rows(const FewRowsArgs& args, bool bf16, bool rcr, bool gated, int num_sms, cudaStream_t stream) {
     FewRowsArgs a = args;
-    const RowsKernel k = rows_kernel((bf16 ? 8 : 0) + (rcr ? 4 : 0) + (gated ? 2 : 0) + (a.M > 8 ? 1 : 0));
+    const RowsKernel k = rows_kernel(bf16, rcr, gated, a.M <= 8 ? 1 : (a.M <= 16 ? 2 : 4));
     const int64_t group = rcr ? 16 : 64, cols = gated ? group : 2 * group;
     const int64_t strips = (a.N + cols - 1) / cols;
-    // split K until most SMs have a block, as long as every warp keeps two
-    // steps
+    // Fewer strips than SMs: split K as many ways as most of the SMs can hold
+    // at once (of clusters of 8 fewer fit: they do not fill a GPC), as long as
+    // every warp keeps a step.  (Clusters that walk
+    // over several strips lose more in their barriers than the evener load
+    // gives: 8192 x 14336, 256 strips, 74 us against 40.)
     const int64_t steps = a.K / (rcr ? 32 : 16);
     int parts = 1;
-    while (parts < 8 && strips * parts < 100 && steps >= 2 * kWarps * (2 * parts)) parts *= 2;
+    while (parts < 8 && strips * 2 * parts <= (parts == 4 ? num_sms * 2 / 3 : num_sms * 7 / 8) &&
+           steps >= kWarps * 2 * parts)
+        parts *= 2;
     a.kparts = parts;
     cudaLaunchConfig_t lc{};
-    const int64_t clusters = strips < num_sms / parts ? strips : num_sms / parts;
+    const int64_t room = static_cast<int64_t>(num_sms) * k.per_sm / parts;
+    const int64_t clusters = strips < room ? strips : room;
     lc.gridDim = dim3(static_cast<unsigned>(clusters * parts), 1, 1);
     lc.blockDim = dim3(32 * kWarps, 1, 1);
     lc.dynamicSmemBytes = k.smem;

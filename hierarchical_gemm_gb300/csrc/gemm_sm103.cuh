@@ -501,85 +501,134 @@ __device__ __forceinline__ void drain_parts(const ParamsFor<kEpi>& p, const CUte
 
 // The gated layer's drain: 32 columns of H at a time, from the gate sums at
 // accumulator column c and the up sums at c + BN / 2, this warpgroup's
-// quarter [c_begin, c_begin + BN / 4) of each.  A unit that holds part of a
-// tile's K range counts the two chunks in together, on the gate chunk's
-// counter; otherwise the parts are added as drain_parts adds them.
+// quarter [c_begin, c_begin + BN / 4) of each.
 template <int BN, int kOut, class Release>
 __device__ __forceinline__ void drain_gated(const FfnParams& p, const CUtensorMap* tmC,
                                             CStager<kOut, kEpiGated>& out, const Unit& un, uint32_t tbase, int row0,
-                                            int row_local, int64_t h, const EpiAux& aux, int c_begin,
-                                            Release&& release) {
+                                            int c_begin, Release&& release) {
     static_assert(BN % 128 == 0, "each warpgroup drains whole 32-column chunks of both halves");
+    const int col0 = un.tn * (BN / 2);
+    const int c_end = c_begin + BN / 4;
+#pragma unroll 1
+    for (int c = c_begin; c < c_end; c += 32) {
+        uint32_t g[32], u[32];
+        tmem_ld_32x32b_x32(tbase + c, g);
+        tmem_ld_32x32b_x32(tbase + c + BN / 2, u);
+        tmem_ld_wait();
+        if (c + 32 >= c_end) release();  // this thread's accumulator part is in registers
+        gated_epilogue(p.epi, row0 + out.lane, p.M, col0 + c, p.N, g, u);
+        out.store(p, tmC, row0, col0 + c, g);
+    }
+}
+
+// r becomes 0 + p_0 + ... + p_{n-1} of one 32-column chunk, this part's own
+// term (in r) at its place.  The others' come two loads ahead of the add, in
+// two passes of 16 columns: with both chunks of a gated pair alive, 32 at a
+// time would spill.
+template <int BN>
+__device__ __forceinline__ void sum_parts(const GemmParams& p, const Unit& un, const EpiAux& aux, int64_t h, int chunk,
+                                          int q, int lane, uint32_t (&r)[32]) {
+    const int n = un.nsplit, me = un.split;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float acc[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
+        float4 pa[4], pb[4];
+        auto fetch = [&](int i, float4 (&x)[4]) {
+            if (i < n - 1) {
+                const float* src = part_chunk<BN>(p, un, aux, h, i < me ? i : i + 1, chunk, q, lane) + half * (4 * 128);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x[v] = ld_global_cg_f4(src + v * 128);
+            }
+        };
+        auto add_own = [&] {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[j] = __fadd_rn(acc[j], __uint_as_float(r[16 * half + j]));
+        };
+        auto add = [&](const float4 (&x)[4]) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                acc[4 * v] = __fadd_rn(acc[4 * v], x[v].x);
+                acc[4 * v + 1] = __fadd_rn(acc[4 * v + 1], x[v].y);
+                acc[4 * v + 2] = __fadd_rn(acc[4 * v + 2], x[v].z);
+                acc[4 * v + 3] = __fadd_rn(acc[4 * v + 3], x[v].w);
+            }
+        };
+        fetch(0, pa);
+        fetch(1, pb);
+#pragma unroll 1
+        for (int i = 0; i < n - 1; i += 2) {
+            if (i == me) add_own();
+            add(pa);
+            fetch(i + 2, pa);
+            if (i + 1 < n - 1) {
+                if (i + 1 == me) add_own();
+                add(pb);
+                fetch(i + 3, pb);
+            }
+        }
+        if (me == n - 1) add_own();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[16 * half + j] = __float_as_uint(acc[j]);
+    }
+}
+
+// The gated drain of a unit that holds part of a tile's K range: as
+// drain_parts, the gate and up chunks of 32 columns of H counted in together
+// on the gate chunk's counter.  The accumulator is read where its values are
+// needed and released at the end, so that no more than one pair of chunks
+// lives in registers.
+template <int BN, int kOut, class Release>
+__device__ __forceinline__ void drain_gated_parts(const FfnParams& p, const CUtensorMap* tmC,
+                                                  CStager<kOut, kEpiGated>& out, const Unit& un, uint32_t tbase,
+                                                  int row0, int row_local, int64_t h, const EpiAux& aux, int c_begin,
+                                                  Release&& release) {
     const int n = un.nsplit, me = un.split;
     const int q = row_local >> 5, lane = row_local & 31;
     const int col0 = un.tn * (BN / 2);
     constexpr int kNc = BN / 128;  // 32-column chunks of H in this warpgroup's part
-    const int first = n > 1 ? me * kNc / n : 0;
+    const int first = me * kNc / n;
 #pragma unroll 1
     for (int k = 0; k < kNc; ++k) {
         int cl = first + k;
         if (cl >= kNc) cl -= kNc;
         const int c = c_begin + cl * 32;
         const int gate = c >> 5, up = (c + BN / 2) >> 5;  // workspace chunks
+        int* cnt = part_counter<BN>(p, h, gate, q);
+        int last = 0;
+        if (lane == 0) last = ld_acquire_gpu(cnt) == n - 1 ? 1 : 0;
+        last = __shfl_sync(0xffffffffu, last, 0);
+        if (!last) {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tbase + c + i * (BN / 2), r);
+                tmem_ld_wait();
+                float* dst = part_chunk<BN>(p, un, aux, h, me, i == 0 ? gate : up, q, lane);
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    st_global_v4(dst + v * 128, r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
+            }
+            __threadfence();  // the partials are visible before they are counted
+            __syncwarp();
+            if (lane == 0) last = atom_acq_rel_gpu_add(cnt, 1) == n - 1 ? 1 : 0;
+            last = __shfl_sync(0xffffffffu, last, 0);
+            if (!last) continue;
+        }
+        __threadfence();  // the other parts' partials, counted in, are read after the count
         uint32_t g[32], u[32];
         tmem_ld_32x32b_x32(tbase + c, g);
+        tmem_ld_wait();
+        sum_parts<BN>(p, un, aux, h, gate, q, lane, g);
         tmem_ld_32x32b_x32(tbase + c + BN / 2, u);
         tmem_ld_wait();
-        if (k == kNc - 1) release();  // this thread's accumulator part is in registers
-        if (n > 1) {
-            int* cnt = part_counter<BN>(p, h, gate, q);
-            int last = 0;
-            if (lane == 0) last = ld_acquire_gpu(cnt) == n - 1 ? 1 : 0;
-            last = __shfl_sync(0xffffffffu, last, 0);
-            if (!last) {
-                float* dg = part_chunk<BN>(p, un, aux, h, me, gate, q, lane);
-                float* du = part_chunk<BN>(p, un, aux, h, me, up, q, lane);
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    st_global_v4(dg + v * 128, g[4 * v], g[4 * v + 1], g[4 * v + 2], g[4 * v + 3]);
-                    st_global_v4(du + v * 128, u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
-                }
-                __threadfence();  // the partials are visible before they are counted
-                __syncwarp();
-                if (lane == 0) last = atom_acq_rel_gpu_add(cnt, 1) == n - 1 ? 1 : 0;
-                last = __shfl_sync(0xffffffffu, last, 0);
-                if (!last) continue;
-            }
-            __threadfence();  // the other parts' partials, counted in, are read after the count
-            // 0 + p_0 + ... + p_{n-1}, this part's own term at its place
-            auto sum = [&](int chunk, uint32_t (&r)[32]) {
-                float acc[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) acc[j] = 0.0f;
-#pragma unroll 1
-                for (int s = 0; s < n; ++s) {
-                    if (s == me) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[j] = __fadd_rn(acc[j], __uint_as_float(r[j]));
-                        continue;
-                    }
-                    const float* src = part_chunk<BN>(p, un, aux, h, s, chunk, q, lane);
-                    float4 x[8];
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) x[v] = ld_global_cg_f4(src + v * 128);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        acc[4 * v] = __fadd_rn(acc[4 * v], x[v].x);
-                        acc[4 * v + 1] = __fadd_rn(acc[4 * v + 1], x[v].y);
-                        acc[4 * v + 2] = __fadd_rn(acc[4 * v + 2], x[v].z);
-                        acc[4 * v + 3] = __fadd_rn(acc[4 * v + 3], x[v].w);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(acc[j]);
-            };
-            sum(gate, g);
-            sum(up, u);
-            if (lane == 0) *reinterpret_cast<volatile int*>(cnt) = 0;  // ready for the next launch
-        }
+        sum_parts<BN>(p, un, aux, h, up, q, lane, u);
+        if (lane == 0) *reinterpret_cast<volatile int*>(cnt) = 0;  // ready for the next launch
         gated_epilogue(p.epi, row0 + lane, p.M, col0 + c, p.N, g, u);
         out.store(p, tmC, row0, col0 + c, g);
     }
+    release();
 }
 
 template <int BN, int kOut, int kEpi, class Release>
@@ -587,7 +636,10 @@ __device__ __forceinline__ void drain_unit(const ParamsFor<kEpi>& p, const CUten
                                            const Unit& un, uint32_t tbase, int row0, int row_local, int64_t h,
                                            const EpiAux& aux, int c_begin, Release&& release) {
     if constexpr (kEpi == kEpiGated) {
-        drain_gated<BN, kOut>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);
+        if (un.nsplit > 1)
+            drain_gated_parts<BN, kOut>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);
+        else
+            drain_gated<BN, kOut>(p, tmC, out, un, tbase, row0, c_begin, release);
     } else {
         if (un.nsplit > 1) {
             drain_parts<BN, kOut, kEpi>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);

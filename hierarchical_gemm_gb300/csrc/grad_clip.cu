@@ -2,16 +2,19 @@
 //
 //   n = sqrt(sum g^2);   out = g min(1, max_norm / (n + 1e-6))
 //
-// Two launches: the first reads every value and sums its square, the last
-// thread block of it to finish adds the blocks' partials in block order and
-// leaves the norm and the coefficient; the second reads again, scales and
-// writes.  HBM bounds both (a multiply-add a value).  The tensors' addresses
-// and sizes travel in the kernel's parameters, so a call copies nothing to
-// the device beforehand.
+// HBM bounds it (a multiply-add a value): every value is read for the norm,
+// and read again and written once the norm is known.  Both passes run in one
+// launch whose blocks are all resident: each leaves the sum of its squares,
+// waits until all have, adds all the sums (in block order, so every block
+// gets the same bits) and scales the values it summed, the last ones first,
+// which L2 still holds.  More tensors than the kernel's parameters list take
+// several launches: one for each list's norm, one for each list's scaling.
+// The tensors' addresses and sizes travel in those parameters, so a call
+// copies nothing to the device beforehand.
 //
-// Squares are summed in fp32 over 32 values and in fp64 from there on.  A
-// group of 8 whose fp32 sum could have overflowed or lost its small squares
-// is summed again in fp64.
+// Squares are summed in fp32 over at most 32 values and in fp64 from there
+// on.  A group of 8 whose fp32 sum could have overflowed or lost its small
+// squares is summed in fp64 by itself.
 #include <cmath>
 
 #include "ffn_epilogue.cuh"
@@ -23,23 +26,38 @@ namespace tsg {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kVecsPerThread = 4;                                       // 16-byte vectors of 8 16-bit values
+constexpr int kVecsPerThread = 4;                                       // groups of 8 values
 constexpr int64_t kChunk = int64_t{kClipThreads} * kVecsPerThread * 8;  // values of a chunk: 8192
-constexpr int kMaxTensors = 512;                                        // per launch (the parameters' size)
+constexpr int kFewTensors = 64, kMaxTensors = 512;                      // of a list
 
+// A list of tensors, cut into chunks.
+template <int kCap>
 struct ClipTable {
-    const void* in[kMaxTensors];
-    void* out[kMaxTensors];
-    int64_t numel[kMaxTensors];
-    int64_t first[kMaxTensors];  // chunks of the tensors before this one
-    uint8_t kind[kMaxTensors];   // ElemKind; bit 7: both addresses 16-byte aligned
+    const void* in[kCap];
+    void* out[kCap];
+    int64_t numel[kCap];
+    int64_t first[kCap];  // chunks of the tensors before this one
+    uint8_t kind[kCap];   // ElemKind; bit 7: both addresses 16-byte aligned
     int32_t count;
+    int32_t in_place;     // every output is its input
     int64_t chunks;
 };
-static_assert(sizeof(ClipTable) + 128 <= 32764, "kernel parameters");
+static_assert(sizeof(ClipTable<kMaxTensors>) + 128 <= 32764, "kernel parameters");
+
+struct ClipSync {
+    double* partials;
+    int* arrived;  // blocks that have left their sum; zero between launches
+    int* left;     // blocks that have read all the sums; zero between launches
+    int* status;
+    uint64_t timeout_ns;
+    float max_norm;
+    float* norm;
+    float* coef;
+};
 
 // The tensor that chunk c belongs to.
-__device__ __forceinline__ int tensor_of(const ClipTable& t, int64_t c) {
+template <class Table>
+__device__ __forceinline__ int tensor_of(const Table& t, int64_t c) {
     int lo = 0, hi = t.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -51,7 +69,8 @@ __device__ __forceinline__ int tensor_of(const ClipTable& t, int64_t c) {
     return lo;
 }
 
-// Values [i, i + 8) of n at p.
+// Values [i, i + 8) of n at p.  (Stores are marked as not read again: what
+// L2 holds of the inputs is worth more.)
 __device__ __forceinline__ void load8_any(int kind, bool aligned, const void* p, int64_t i, int64_t n, float (&v)[8]) {
     if (aligned) {
         load8(kind, p, i, n, v);
@@ -69,15 +88,14 @@ __device__ __forceinline__ void store8_any(int kind, bool aligned, void* p, int6
     if (aligned && i + 8 <= n) {
         if (kind == kElemF32) {
             float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-            d[0] = make_float4(v[0], v[1], v[2], v[3]);
-            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            __stcs(d, make_float4(v[0], v[1], v[2], v[3]));
+            __stcs(d + 1, make_float4(v[4], v[5], v[6], v[7]));
         } else {
-            uint4 w;
-            uint32_t* x = &w.x;
+            uint32_t x[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 x[j] = kind == kElemBF16 ? pack16<true>(v[2 * j], v[2 * j + 1]) : pack16<false>(v[2 * j], v[2 * j + 1]);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = w;
+            __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i), make_uint4(x[0], x[1], x[2], x[3]));
         }
         return;
     }
@@ -106,84 +124,211 @@ __device__ __forceinline__ double block_sum(double x) {
     return s;
 }
 
-// Chunks blockIdx.x, blockIdx.x + gridDim.x, ...; this launch's partials
-// start at `base`, `total` of them come from all launches, and the last
-// launch (`final`) makes the norm.
-__global__ void __launch_bounds__(kClipThreads) clip_norm_sm103(const __grid_constant__ ClipTable t, double* partials,
-                                                                int base, int total, int final, int* counter,
-                                                                float max_norm, float* norm, float* coef) {
-    double acc = 0.0;
-    for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const int k = tensor_of(t, c);
-        const int kind = t.kind[k] & 0x7f;
-        const bool aligned = t.kind[k] & 0x80;
-        const int64_t n = t.numel[k], at = (c - t.first[k]) * kChunk + threadIdx.x * 8;
-        float s = 0.0f;
+// Adds the squares of 8 values: to s, or, where fp32 could not hold them, to
+// acc.
+__device__ __forceinline__ void add_squares(const float (&x)[8], float& s, double& acc) {
+    float q = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q = fmaf(x[j], x[j], q);
+    if (q > 1e37f || q < 1e-30f) {
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+        if (top > 0.0f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc += static_cast<double>(x[j]) * static_cast<double>(x[j]);
+        }
+    } else {
+        s += q;  // (a NaN comes through here)
+    }
+}
+
+// This thread's groups of 8 values in chunk c, handed to f.  kLast: they are
+// not read again, so L2 need not keep them.
+template <bool kLast, class Table, class F>
+__device__ __forceinline__ void with_chunk(const Table& t, int64_t c, F&& f) {
+    const int k = tensor_of(t, c);
+    const int kind = t.kind[k] & 0x7f;
+    const bool aligned = t.kind[k] & 0x80;
+    const int64_t n = t.numel[k], start = (c - t.first[k]) * kChunk, at = start + threadIdx.x * 8;
+    float x[kVecsPerThread][8];
+    if (aligned && start + kChunk <= n && kind != kElemF32) {
+        // a whole chunk of 16-bit values: every load before the first use
+        uint4 w[kVecsPerThread];
+#pragma unroll
+        for (int v = 0; v < kVecsPerThread; ++v)
+        {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.in[k]) + at) + v * kClipThreads;
+            w[v] = kLast ? __ldcs(p) : *p;
+        }
+#pragma unroll
+        for (int v = 0; v < kVecsPerThread; ++v) {
+            const uint32_t r[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 y = kind == kElemBF16 ? unpack16<true>(r[j]) : unpack16<false>(r[j]);
+                x[v][2 * j] = y.x;
+                x[v][2 * j + 1] = y.y;
+            }
+        }
+    } else {
 #pragma unroll
         for (int v = 0; v < kVecsPerThread; ++v) {
             const int64_t i = at + v * (kClipThreads * 8);
-            if (i >= n) break;
-            float x[8], q = 0.0f;
-            load8_any(kind, aligned, t.in[k], i, n, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q = fmaf(x[j], x[j], q);
-            if (q > 1e37f || q < 1e-30f) {
-                float top = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-                if (top > 0.0f) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc += static_cast<double>(x[j]) * static_cast<double>(x[j]);
-                }
+            if (i < n) {
+                load8_any(kind, aligned, t.in[k], i, n, x[v]);
             } else {
-                s += q;  // (a NaN comes through here)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[v][j] = 0.0f;
             }
         }
-        acc += static_cast<double>(s);
     }
-    const double mine = block_sum(acc);
+    f(x, k, kind, aligned, at, n);
+}
+
+template <class Table>
+__device__ __forceinline__ double sum_chunks(const Table& t) {
+    double acc = 0.0;
+    for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+        with_chunk<false>(t, c, [&](const float (&x)[kVecsPerThread][8], int, int, bool, int64_t, int64_t) {
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kVecsPerThread; ++v) add_squares(x[v], s, acc);
+            acc += static_cast<double>(s);
+        });
+    }
+    return block_sum(acc);
+}
+
+// The last of this block's chunks first: the first pass read them last.
+template <class Table>
+__device__ __forceinline__ void scale_chunks(const Table& t, float f) {
+    if (t.chunks <= blockIdx.x) return;
+    const int64_t last = blockIdx.x + (t.chunks - 1 - blockIdx.x) / gridDim.x * gridDim.x;
+    for (int64_t c = last; c >= 0; c -= gridDim.x) {
+        with_chunk<true>(t, c, [&](float (&x)[kVecsPerThread][8], int k, int kind, bool aligned, int64_t at, int64_t n) {
+#pragma unroll
+            for (int v = 0; v < kVecsPerThread; ++v) {
+                const int64_t i = at + v * (kClipThreads * 8);
+                if (i >= n) break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[v][j] *= f;
+                store8_any(kind, aligned, t.out[k], i, n, x[v]);
+            }
+        });
+    }
+}
+
+// Norm and coefficient from the sum of all squares.
+__device__ __forceinline__ float clip_coef(double sum, float max_norm, float* norm) {
+    const double n = sqrt(sum);
+    if (norm) *norm = static_cast<float>(n);
+    double f = static_cast<double>(max_norm) / (n + 1e-6);
+    if (f > 1.0) f = 1.0;  // (a NaN stays one)
+    return static_cast<float>(f);
+}
+
+__device__ __forceinline__ double sum_partials(const double* partials, int n) {
+    double x = 0.0;
+    for (int i = threadIdx.x; i < n; i += kClipThreads) x += __ldcg(partials + i);
+    return block_sum(x);
+}
+
+// One launch for everything; all blocks resident (a cooperative launch).
+template <int kCap>
+__global__ void __launch_bounds__(kClipThreads, 4) clip_sm103(const __grid_constant__ ClipTable<kCap> t,
+                                                              const ClipSync y) {
+    const double mine = sum_chunks(t);
+    __shared__ int ok;
+    const int blocks = static_cast<int>(gridDim.x);
+    if (threadIdx.x == 0) {
+        y.partials[blockIdx.x] = mine;
+        int seen = atom_acq_rel_gpu_add(y.arrived, 1) + 1;
+        const uint64_t t0 = globaltimer();
+        while (seen < blocks && globaltimer() - t0 <= y.timeout_ns) seen = ld_acquire_gpu(y.arrived);
+        ok = seen >= blocks;
+        if (!ok) atomicExch(y.status, 5 /* TSGEMM_ERR_TIMEOUT */);
+    }
+    __syncthreads();
+    if (!ok) return;
+    __threadfence();
+    const double sum = sum_partials(y.partials, blocks);
+    const float f = clip_coef(sum, y.max_norm, blockIdx.x == 0 && threadIdx.x == 0 ? y.norm : nullptr);
+    if (threadIdx.x == 0 && atom_acq_rel_gpu_add(y.left, 1) == blocks - 1) {
+        // no block reads the counters any more: ready for the next launch
+        *y.arrived = 0;
+        *y.left = 0;
+    }
+    if (t.in_place && f == 1.0f) return;  // nothing to change
+    scale_chunks(t, f);
+}
+
+// The same in several launches.  This launch's sums start at `base`, `total`
+// of them come from all launches, and the last one (`final`) makes the norm.
+__global__ void __launch_bounds__(kClipThreads) clip_norm_sm103(const __grid_constant__ ClipTable<kMaxTensors> t,
+                                                                const ClipSync y, int base, int total, int final) {
+    const double mine = sum_chunks(t);
     __shared__ int is_last;
     if (threadIdx.x == 0) {
-        partials[base + blockIdx.x] = mine;
+        y.partials[base + blockIdx.x] = mine;
         is_last = 0;
-        if (final) is_last = atom_acq_rel_gpu_add(counter, 1) == static_cast<int>(gridDim.x) - 1;
+        if (final) is_last = atom_acq_rel_gpu_add(y.arrived, 1) == static_cast<int>(gridDim.x) - 1;
     }
     __syncthreads();
     if (!is_last) return;
     __threadfence();
-    double x = 0.0;
-    for (int i = threadIdx.x; i < total; i += kClipThreads) x += __ldcg(partials + i);
-    x = block_sum(x);
+    const double sum = sum_partials(y.partials, total);
     if (threadIdx.x == 0) {
-        const double n = sqrt(x);
-        *norm = static_cast<float>(n);
-        double f = static_cast<double>(max_norm) / (n + 1e-6);
-        if (f > 1.0) f = 1.0;  // (a NaN stays one)
-        *coef = static_cast<float>(f);
-        *counter = 0;  // ready for the next launch
+        *y.coef = clip_coef(sum, y.max_norm, y.norm);
+        *y.arrived = 0;  // ready for the next launch
     }
 }
-
-__global__ void __launch_bounds__(kClipThreads) clip_scale_sm103(const __grid_constant__ ClipTable t,
-                                                                 const float* coef, int in_place) {
+__global__ void __launch_bounds__(kClipThreads) clip_scale_sm103(const __grid_constant__ ClipTable<kMaxTensors> t,
+                                                                 const float* coef) {
     const float f = *coef;
-    if (in_place && f == 1.0f) return;  // nothing to change
-    for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const int k = tensor_of(t, c);
-        const int kind = t.kind[k] & 0x7f;
-        const bool aligned = t.kind[k] & 0x80;
-        const int64_t n = t.numel[k], at = (c - t.first[k]) * kChunk + threadIdx.x * 8;
-#pragma unroll
-        for (int v = 0; v < kVecsPerThread; ++v) {
-            const int64_t i = at + v * (kClipThreads * 8);
-            if (i >= n) break;
-            float x[8];
-            load8_any(kind, aligned, t.in[k], i, n, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= f;
-            store8_any(kind, aligned, t.out[k], i, n, x);
-        }
+    if (t.in_place && f == 1.0f) return;  // nothing to change
+    scale_chunks(t, f);
+}
+
+// The tensors from `from` on that fit the table (empty ones take no place);
+// returns the first that does not.
+template <int kCap>
+int64_t fill(ClipTable<kCap>& t, int64_t from, int64_t count, const void* const* grads, void* const* out,
+             const int64_t* numel, const int32_t* dtype) {
+    t.count = 0;
+    t.chunks = 0;
+    t.in_place = 1;
+    int64_t i = from;
+    for (; i < count; ++i) {
+        if (numel[i] == 0) continue;
+        if (t.count == kCap) break;
+        const int k = t.count++;
+        t.in[k] = grads[i];
+        t.out[k] = out[i];
+        t.numel[k] = numel[i];
+        t.first[k] = t.chunks;
+        t.chunks += (numel[i] + kChunk - 1) / kChunk;
+        const bool aligned = ((reinterpret_cast<uintptr_t>(grads[i]) | reinterpret_cast<uintptr_t>(out[i])) & 15u) == 0;
+        const int kind = dtype[i] == TSGEMM_F32 ? kElemF32 : (dtype[i] == TSGEMM_BF16 ? kElemBF16 : kElemF16);
+        t.kind[k] = static_cast<uint8_t>(kind | (aligned ? 0x80 : 0));
+        if (grads[i] != out[i]) t.in_place = 0;
     }
+    return i;
+}
+
+template <int kCap>
+cudaError_t launch_one(const ClipTable<kCap>& t, const ClipSync& y, int num_sms, cudaStream_t stream) {
+    cudaLaunchConfig_t lc{};
+    const int64_t most = static_cast<int64_t>(num_sms) * 4;  // resident: see the launch bounds
+    lc.gridDim = dim3(static_cast<unsigned>(t.chunks < 1 ? 1 : (t.chunks < most ? t.chunks : most)), 1, 1);
+    lc.blockDim = dim3(kClipThreads, 1, 1);
+    lc.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, clip_sm103<kCap>, t, y);
 }
 
 }  // namespace
@@ -191,54 +336,37 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_sm103(const __grid_co
 cudaError_t launch_clip(int64_t count, const void* const* grads, void* const* out, const int64_t* numel,
                         const int32_t* dtype, float max_norm, float* norm, const ClipScratch& scratch, int num_sms,
                         cudaStream_t stream) {
-    ClipTable t;
-    const int64_t most_blocks = static_cast<int64_t>(num_sms) * 8;
-    auto fill = [&](int64_t from, bool* in_place) {
-        t.count = 0;
-        t.chunks = 0;
-        *in_place = true;
-        int64_t i = from;
-        for (; i < count && t.count < kMaxTensors; ++i) {
-            if (numel[i] == 0) continue;
-            const int k = t.count++;
-            t.in[k] = grads[i];
-            t.out[k] = out[i];
-            t.numel[k] = numel[i];
-            t.first[k] = t.chunks;
-            t.chunks += (numel[i] + kChunk - 1) / kChunk;
-            const bool aligned =
-                ((reinterpret_cast<uintptr_t>(grads[i]) | reinterpret_cast<uintptr_t>(out[i])) & 15u) == 0;
-            const int kind = dtype[i] == TSGEMM_F32 ? kElemF32 : (dtype[i] == TSGEMM_BF16 ? kElemBF16 : kElemF16);
-            t.kind[k] = static_cast<uint8_t>(kind | (aligned ? 0x80 : 0));
-            if (grads[i] != out[i]) *in_place = false;
-        }
-        return i;
-    };
-    auto blocks = [&](int64_t limit) {
-        const int64_t b = t.chunks < limit ? t.chunks : limit;
-        return static_cast<int>(b < 1 ? 1 : b);
-    };
-    // launches of kMaxTensors non-empty tensors each; their partials share
-    // the scratch
-    int64_t tables = 0;
-    bool same = true;
-    for (int64_t i = 0; i < count || tables == 0; ++tables) i = fill(i, &same);
-    int64_t per = scratch.max_partials / tables;
+    const ClipSync y{scratch.partials, scratch.counters, scratch.counters + 1, scratch.status, scratch.timeout_ns,
+                     max_norm,         norm,             scratch.coef};
+    if (count <= kFewTensors) {
+        ClipTable<kFewTensors> t;
+        fill(t, 0, count, grads, out, numel, dtype);
+        return launch_one(t, y, num_sms, stream);
+    }
+    ClipTable<kMaxTensors> t;
+    int64_t i = fill(t, 0, count, grads, out, numel, dtype);
+    if (i == count) return launch_one(t, y, num_sms, stream);
+    int64_t lists = 1;
+    for (; i < count; ++lists) i = fill(t, i, count, grads, out, numel, dtype);
+    const int64_t most = static_cast<int64_t>(num_sms) * 4;
+    int64_t per = scratch.max_partials / lists;
     if (per < 1) return cudaErrorInvalidValue;
-    if (per > most_blocks) per = most_blocks;
+    if (per > most) per = most;
+    auto blocks = [&](int64_t limit) {
+        return static_cast<int>(t.chunks < 1 ? 1 : (t.chunks < limit ? t.chunks : limit));
+    };
     int base = 0;
-    int64_t i = 0;
-    for (int64_t k = 0; k < tables; ++k) {
-        i = fill(i, &same);
+    i = 0;
+    for (int64_t k = 0; k < lists; ++k) {
+        i = fill(t, i, count, grads, out, numel, dtype);
         const int b = blocks(per);
-        clip_norm_sm103<<<b, kClipThreads, 0, stream>>>(t, scratch.partials, base, base + b, k == tables - 1,
-                                                        scratch.counter, max_norm, norm, scratch.coef);
+        clip_norm_sm103<<<b, kClipThreads, 0, stream>>>(t, y, base, base + b, k == lists - 1);
         base += b;
     }
     i = 0;
-    for (int64_t k = 0; k < tables; ++k) {
-        i = fill(i, &same);
-        if (t.chunks) clip_scale_sm103<<<blocks(most_blocks), kClipThreads, 0, stream>>>(t, scratch.coef, same ? 1 : 0);
+    for (int64_t k = 0; k < lists; ++k) {
+        i = fill(t, i, count, grads, out, numel, dtype);
+        clip_scale_sm103<<<blocks(most), kClipThreads, 0, stream>>>(t, scratch.coef);
     }
     return cudaGetLastError();
 }

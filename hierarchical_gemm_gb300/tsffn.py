@@ -17,10 +17,14 @@ Calls run on the current stream (or `stream`) with a workspace that belongs
 to that stream: see handle().
 """
 import ctypes
+import struct
 from array import array
 
-from .tsgemm import (BF16, F16, F32, LAYOUT_RCR, LAYOUT_RRR, _check, _stream_handle, dtype_code, lib, status_string)
+import torch
 
+from .tsgemm import BF16, F16, F32, LAYOUT_RCR, LAYOUT_RRR, OK, TsgemmError, _check, lib, status_string
+
+_DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_SIGMOID = range(6)
 _ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU,
          "sigmoid": ACT_SIGMOID}
@@ -60,6 +64,16 @@ class GatedBackwardArgs(ctypes.Structure):
                        "lddh ldx ldw lddx lddw")
 
 
+def _packer(cls):
+    """The structure's bytes from its fields in order (cheaper to fill than
+    the ctypes object; native alignment is what the C compiler does)."""
+    code = {_i64: "q", _i32: "i", _vp: "P"}
+    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
+
+
+_pack_linear, _pack_linear_backward = _packer(LinearArgs), _packer(LinearBackwardArgs)
+_pack_gated, _pack_gated_backward = _packer(GatedArgs), _packer(GatedBackwardArgs)
+
 lib.tsffn_create.restype = _i32
 lib.tsffn_create.argtypes = [ctypes.POINTER(_vp)]
 for _name in ("tsffn_destroy", "tsffn_status"):
@@ -78,21 +92,19 @@ class Handle:
     captured into included)."""
 
     def __init__(self):
-        self._h = _vp()
-        _check(lib.tsffn_create(ctypes.byref(self._h)), "tsffn_create")
-
-    @property
-    def raw(self):
-        return self._h.value
+        h = _vp()
+        self.raw = None
+        _check(lib.tsffn_create(ctypes.byref(h)), "tsffn_create")
+        self.raw = h.value
 
     def status(self):
         """Device status word after the calls have completed (0 = OK)."""
-        return lib.tsffn_status(self._h)
+        return lib.tsffn_status(self.raw)
 
     def close(self):
-        if self._h:
-            lib.tsffn_destroy(self._h)
-            self._h = _vp()
+        if self.raw:
+            lib.tsffn_destroy(self.raw)
+            self.raw = None
 
     def __del__(self):
         try:
@@ -104,13 +116,20 @@ class Handle:
 _handles = {}
 
 
+def _stream(stream):
+    """(raw stream, device): the given stream or the current one."""
+    dev = torch._C._cuda_getDevice()
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev), dev
+    return (stream if isinstance(stream, int) else stream.cuda_stream), dev
+
+
 def handle(stream=None):
     """The handle of a stream (default: the current one) of the current
     device, made on first use and kept.  To replay a captured graph beside
     eager calls, capture it with a Handle() of its own (`handle=`)."""
-    import torch
-    s = _stream_handle(stream)
-    key = (torch.cuda.current_device(), s)
+    torch.cuda.init()
+    key = _stream(stream)
     h = _handles.get(key)
     if h is None:
         h = _handles[key] = Handle()
@@ -122,20 +141,36 @@ def status(stream=None):
     return handle(stream).status()
 
 
+def _run(fn, what, args, stream, h):
+    key = _stream(stream)
+    if h is None:
+        h = _handles.get(key) or handle(stream)
+    code = fn(h.raw, args, key[0])
+    if code != OK:
+        raise TsgemmError(code, what)
+
+
 def _act(act):
-    if isinstance(act, int):
-        return act
-    try:
-        return _ACTS[act]
-    except KeyError:
-        raise ValueError("unknown activation %r" % (act,)) from None
+    code = _ACTS.get(act)
+    if code is None:
+        if isinstance(act, int):
+            return act
+        raise ValueError("unknown activation %r" % (act,))
+    return code
+
+
+def _dtype(t, what):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float16, bfloat16 or (where it may) float32" % what)
+    return code
 
 
 def _rows(t, what):
     """Row stride of a 2-D tensor with unit stride along its rows."""
-    r, c = t.shape
     s0, s1 = t.stride()
-    if c > 1 and s1 != 1:
+    r, c = t.shape
+    if s1 != 1 and c > 1:
         raise ValueError("%s must have unit stride along its rows" % what)
     if r == 1:  # the stride of a single row says nothing
         return (c + 7) // 8 * 8
@@ -155,9 +190,9 @@ def _weights(W, what):
 
 def _empty(rows, cols, dtype, device):
     """rows x cols with rows that start on 16-byte boundaries."""
-    import torch
-    ld = (cols + 7) // 8 * 8
-    return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols]
+    if cols % 8 == 0:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    return torch.empty((rows, (cols + 7) // 8 * 8), dtype=dtype, device=device)[:, :cols]
 
 
 def _empty_weights(W, layout, dtype):
@@ -168,31 +203,42 @@ def _empty_weights(W, layout, dtype):
     return _empty(K, N, dtype, W.device)
 
 
-def _shape(t, shape, what):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must be %s" % (what, " x ".join(map(str, shape))))
+def _mat(t, rows, cols, dtype, what):
+    """(address, row stride) of a rows x cols tensor of `dtype`."""
+    if t.shape != (rows, cols):
+        raise ValueError("%s must be %d x %d" % (what, rows, cols))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s" % (what, dtype))
+    return t.data_ptr(), _rows(t, what)
 
 
 def _vec(t, n, what):
-    if t is not None and (tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1)):
+    """(address, type) of a contiguous vector."""
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous vector of %d" % (what, n))
+    return t.data_ptr(), _dtype(t, what)
 
 
-def _same(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise ValueError("%s must be %s, as X is" % (name, dtype))
+def _operands(X, W):
+    """Sizes, type, layout and strides of X (M x K) and W (K x N)."""
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("expected X (M x K) and W (K x N)")
+    M, K = X.shape
+    Kw, N = W.shape
+    if K != Kw:
+        raise ValueError("expected X (M x K) and W (K x N)")
+    if X.dtype != W.dtype:
+        raise ValueError("X and W must have the same dtype")
+    layout, ldw = _weights(W, "W")
+    return M, N, K, _dtype(X, "X"), layout, _rows(X, "X"), ldw
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _saved_ok(saved, rows, cols):
-    import torch
-    if saved is not None and (saved.dtype != torch.float32 or tuple(saved.shape) != (rows, cols) or
-                              not saved.is_contiguous()):
+def _saved(saved, rows, cols):
+    if saved is None:
+        raise ValueError("saved is needed: what the forward pass returned with save=True")
+    if saved.dtype != torch.float32 or saved.shape != (rows, cols) or not saved.is_contiguous():
         raise ValueError("saved must be the contiguous %d x %d float32 tensor of the forward pass" % (rows, cols))
+    return saved.data_ptr()
 
 
 def linear(X, W, bias=None, act="none", residual=None, C=None, out_dtype=None, save=False, stream=None, handle=None):
@@ -205,33 +251,20 @@ def linear(X, W, bias=None, act="none", residual=None, C=None, out_dtype=None, s
     With `save`, returns (C, saved) for linear_backward: the float32
     pre-activations X W + bias, in rows padded to a multiple of 8, or None
     without an activation, whose backward pass needs none."""
-    import torch
-    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[0]:
-        raise ValueError("expected X (M x K) and W (K x N)")
-    M, K = X.shape
-    N = W.shape[1]
-    _same(X.dtype, W=W)
+    M, N, K, din, layout, ldx, ldw = _operands(X, W)
     code = _act(act)
     if C is None:
         C = _empty(M, N, X.dtype if out_dtype is None else out_dtype, X.device)
-    _shape(C, (M, N), "C")
-    if out_dtype is not None and C.dtype != out_dtype:
-        raise ValueError("C is not of out_dtype")
-    _shape(residual, (M, N), "residual")
-    if residual is not None and residual.dtype != C.dtype:
-        raise ValueError("residual must have C's dtype")
-    _vec(bias, N, "bias")
-    layout, ldw = _weights(W, "W")
-    saved = None
+    c, ldc = _mat(C, M, N, C.dtype if out_dtype is None else out_dtype, "C")
+    r, ldr = (0, 0) if residual is None else _mat(residual, M, N, C.dtype, "residual")
+    b, dbias = (0, din) if bias is None else _vec(bias, N, "bias")
+    saved, z = None, 0
     if save and code != ACT_NONE:
         saved = torch.empty((M, (N + 7) // 8 * 8), dtype=torch.float32, device=X.device)
-    din = dtype_code(X.dtype)
-    args = LinearArgs(M, N, K, din, dtype_code(C.dtype), din if bias is None else dtype_code(bias.dtype), layout, code,
-                      0, X.data_ptr(), W.data_ptr(), _p(bias), _p(residual), C.data_ptr(), _p(saved), _rows(X, "X"),
-                      ldw, 0 if residual is None else _rows(residual, "residual"), _rows(C, "C"))
-    s = _stream_handle(stream)
-    h = handle if handle is not None else _handle_of(s)
-    _check(lib.tsffn_linear(h.raw, ctypes.byref(args), s), "tsffn_linear")
+        z = saved.data_ptr()
+    _run(lib.tsffn_linear, "tsffn_linear",
+         _pack_linear(M, N, K, din, _dtype(C, "C"), dbias, layout, code, 0, X.data_ptr(), W.data_ptr(), b, r, c, z, ldx,
+                      ldw, ldr, ldc), stream, handle)
     return (C, saved) if save else C
 
 
@@ -244,43 +277,22 @@ def linear_backward(dC, X, W, saved=None, act="none", dX=None, dW=None, dbias=No
     are written; of the others those named in `need` ("dX", "dW", "dbias")
     are made, dW stored as W is, and the rest are None.  dW and dbias may be
     float32."""
-    import torch
-    if dC.dim() != 2 or X.dim() != 2 or W.dim() != 2:
-        raise ValueError("expected dC (M x N), X (M x K) and W (K x N)")
-    M, N = dC.shape
-    K = X.shape[1]
-    _shape(X, (M, K), "X")
-    _shape(W, (K, N), "W")
-    _same(X.dtype, W=W, dC=dC, dX=dX)
+    M, N, K, din, layout, ldx, ldw = _operands(X, W)
     code = _act(act)
-    layout, ldw = _weights(W, "W")
-    if dX is None and "dX" in need:
-        dX = _empty(M, K, X.dtype, X.device)
-    if dW is None and "dW" in need:
-        dW = _empty_weights(W, layout, dw_dtype or X.dtype)
+    if dC.dim() != 2:
+        raise ValueError("expected dC (M x N)")
+    dc, lddc = _mat(dC, M, N, X.dtype, "dC")
+    z = 0 if code == ACT_NONE else _saved(saved, M, (N + 7) // 8 * 8)
+    dX, dx, lddx, dW, dw, ddw, lddw = _gradients(X, W, layout, dX, dW, need, dw_dtype)
     if dbias is None and "dbias" in need:
         dbias = torch.empty(N, dtype=X.dtype, device=X.device)
-    _shape(dX, (M, K), "dX")
-    _shape(dW, (K, N), "dW")
-    _vec(dbias, N, "dbias")
-    lddw = _like_weights(dW, layout)
-    ldz = (N + 7) // 8 * 8
-    if code == ACT_NONE:
-        saved = None
-    elif saved is None:
-        raise ValueError("saved is needed with an activation")
-    _saved_ok(saved, M, ldz)
+    db, ddb = (0, din) if dbias is None else _vec(dbias, N, "dbias")
     ws = None
-    if code != ACT_NONE and (dX is not None or dW is not None):
-        ws = torch.empty((M, ldz), dtype=X.dtype, device=X.device)
-    din = dtype_code(X.dtype)
-    args = LinearBackwardArgs(M, N, K, din, din if dW is None else dtype_code(dW.dtype),
-                              din if dbias is None else dtype_code(dbias.dtype), layout, code, 0, dC.data_ptr(),
-                              X.data_ptr(), W.data_ptr(), _p(saved), _p(dX), _p(dW), _p(dbias), _p(ws),
-                              _rows(dC, "dC"), _rows(X, "X"), ldw, 0 if dX is None else _rows(dX, "dX"), lddw)
-    s = _stream_handle(stream)
-    h = handle if handle is not None else _handle_of(s)
-    _check(lib.tsffn_linear_backward(h.raw, ctypes.byref(args), s), "tsffn_linear_backward")
+    if code != ACT_NONE and (dx or dw):
+        ws = torch.empty((M, (N + 7) // 8 * 8), dtype=X.dtype, device=X.device)
+    _run(lib.tsffn_linear_backward, "tsffn_linear_backward",
+         _pack_linear_backward(M, N, K, din, ddw, ddb, layout, code, 0, dc, X.data_ptr(), W.data_ptr(), z, dx, dw, db,
+                               0 if ws is None else ws.data_ptr(), lddc, ldx, ldw, lddx, lddw), stream, handle)
     return dX, dW, dbias
 
 
@@ -291,23 +303,17 @@ def gated(X, W, act="silu", H=None, save=False, stream=None, handle=None):
 
     With `save`, returns (H, saved) for gated_backward: the float32 products
     (M x 2F)."""
-    import torch
-    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[0] or W.shape[1] % 2:
+    M, N, K, din, layout, ldx, ldw = _operands(X, W)
+    if N % 2:
         raise ValueError("expected X (M x K) and W (K x 2F)")
-    M, K = X.shape
-    F = W.shape[1] // 2
-    _same(X.dtype, W=W, H=H)
-    code = _act(act)
+    F = N // 2
     if H is None:
         H = _empty(M, F, X.dtype, X.device)
-    _shape(H, (M, F), "H")
-    layout, ldw = _weights(W, "W")
-    saved = torch.empty((M, 2 * F), dtype=torch.float32, device=X.device) if save else None
-    args = GatedArgs(M, F, K, dtype_code(X.dtype), layout, code, 0, X.data_ptr(), W.data_ptr(), H.data_ptr(),
-                     _p(saved), _rows(X, "X"), ldw, _rows(H, "H"))
-    s = _stream_handle(stream)
-    h = handle if handle is not None else _handle_of(s)
-    _check(lib.tsffn_gated(h.raw, ctypes.byref(args), s), "tsffn_gated")
+    h, ldh = _mat(H, M, F, X.dtype, "H")
+    saved = torch.empty((M, N), dtype=torch.float32, device=X.device) if save else None
+    _run(lib.tsffn_gated, "tsffn_gated",
+         _pack_gated(M, F, K, din, layout, _act(act), 0, X.data_ptr(), W.data_ptr(), h,
+                     saved.data_ptr() if save else 0, ldx, ldw, ldh), stream, handle)
     return (H, saved) if save else H
 
 
@@ -315,34 +321,17 @@ def gated_backward(dH, X, W, saved, act="silu", dX=None, dW=None, need=("dX", "d
                    handle=None):
     """Gradients of gated(X, W, act): (dX, dW) for the gradient dH (M x F) of
     its result; `saved`, `need` and `dw_dtype` as for linear_backward."""
-    import torch
-    if dH.dim() != 2 or X.dim() != 2 or W.dim() != 2:
+    M, N, K, din, layout, ldx, ldw = _operands(X, W)
+    if N % 2 or dH.dim() != 2:
         raise ValueError("expected dH (M x F), X (M x K) and W (K x 2F)")
-    M, F = dH.shape
-    K = X.shape[1]
-    _shape(X, (M, K), "X")
-    _shape(W, (K, 2 * F), "W")
-    _same(X.dtype, W=W, dH=dH, dX=dX)
-    code = _act(act)
-    layout, ldw = _weights(W, "W")
-    if dX is None and "dX" in need:
-        dX = _empty(M, K, X.dtype, X.device)
-    if dW is None and "dW" in need:
-        dW = _empty_weights(W, layout, dw_dtype or X.dtype)
-    _shape(dX, (M, K), "dX")
-    _shape(dW, (K, 2 * F), "dW")
-    lddw = _like_weights(dW, layout)
-    if saved is None:
-        raise ValueError("saved is needed")
-    _saved_ok(saved, M, 2 * F)
-    ws = torch.empty((M, 2 * F), dtype=X.dtype, device=X.device)
-    din = dtype_code(X.dtype)
-    args = GatedBackwardArgs(M, F, K, din, din if dW is None else dtype_code(dW.dtype), layout, code, dH.data_ptr(),
-                             X.data_ptr(), W.data_ptr(), saved.data_ptr(), _p(dX), _p(dW), ws.data_ptr(),
-                             _rows(dH, "dH"), _rows(X, "X"), ldw, 0 if dX is None else _rows(dX, "dX"), lddw)
-    s = _stream_handle(stream)
-    h = handle if handle is not None else _handle_of(s)
-    _check(lib.tsffn_gated_backward(h.raw, ctypes.byref(args), s), "tsffn_gated_backward")
+    F = N // 2
+    dh, lddh = _mat(dH, M, F, X.dtype, "dH")
+    z = _saved(saved, M, N)
+    dX, dx, lddx, dW, dw, ddw, lddw = _gradients(X, W, layout, dX, dW, need, dw_dtype)
+    ws = torch.empty((M, N), dtype=X.dtype, device=X.device)
+    _run(lib.tsffn_gated_backward, "tsffn_gated_backward",
+         _pack_gated_backward(M, F, K, din, ddw, layout, _act(act), dh, X.data_ptr(), W.data_ptr(), z, dx, dw,
+                              ws.data_ptr(), lddh, ldx, ldw, lddx, lddw), stream, handle)
     return dX, dW
 
 
@@ -352,50 +341,63 @@ def clip_grad_norm(grads, max_norm, out=None, norm=None, stream=None, handle=Non
     place or into the tensors `out` (same sizes and types).  Returns n as a
     float32 tensor on the device (`norm`, if given: one value); the host does
     not wait for it."""
-    import torch
     grads = list(grads)
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError("out must have a tensor for each of grads")
-    for g in grads:
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
+    # (one pass per property, over whole lists: a training step may have
+    # hundreds of gradients)
+    dtypes = [g.dtype for g in grads]
+    sizes = list(map(_numel, grads))
+    if not all(map(_is_contiguous, grads)):
+        raise ValueError("gradients must be contiguous")
+    try:
+        kinds = array("i", map(_DTYPES.__getitem__, dtypes))
+    except KeyError:
+        raise ValueError("gradients must be float16, bfloat16 or float32") from None
+    ins = array("Q", map(_data_ptr, grads))
+    to = ins
     if out is not None:
-        for g, o in zip(grads, outs):
-            if o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous():
-                raise ValueError("each of out must be contiguous, of its gradient's size and type")
+        if [o.dtype for o in outs] != dtypes or list(map(_numel, outs)) != sizes or not all(map(_is_contiguous, outs)):
+            raise ValueError("each of out must be contiguous, of its gradient's size and type")
+        to = array("Q", map(_data_ptr, outs))
+    sizes = array("q", sizes)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=grads[0].device if grads else "cuda")
     elif norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be one float32 value")
-    codes = {}
-    kinds = array("i")
-    for g in grads:
-        k = codes.get(g.dtype)
-        if k is None:
-            k = codes[g.dtype] = dtype_code(g.dtype)
-        kinds.append(k)
-    ins = array("Q", [g.data_ptr() for g in grads])
-    to = ins if out is None else array("Q", [o.data_ptr() for o in outs])
-    sizes = array("q", [g.numel() for g in grads])
-    s = _stream_handle(stream)
-    h = handle if handle is not None else _handle_of(s)
-    _check(lib.tsffn_clip_grad_norm(h.raw, len(grads), ins.buffer_info()[0], to.buffer_info()[0],
-                                    sizes.buffer_info()[0], kinds.buffer_info()[0], float(max_norm), norm.data_ptr(),
-                                    s), "tsffn_clip_grad_norm")
+    key = _stream(stream)
+    if handle is None:
+        handle = _handles.get(key) or _make_handle(stream)
+    _check(lib.tsffn_clip_grad_norm(handle.raw, len(grads), ins.buffer_info()[0], to.buffer_info()[0],
+                                    sizes.buffer_info()[0], kinds.buffer_info()[0], max_norm, norm.data_ptr(),
+                                    key[0]), "tsffn_clip_grad_norm")
     return norm
 
 
-def _handle_of(s):
-    import torch
-    h = _handles.get((torch.cuda.current_device(), s))
-    return h if h is not None else handle(s)
+_make_handle = handle
+_numel, _is_contiguous, _data_ptr = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
+
+
+def _gradients(X, W, layout, dX, dW, need, dw_dtype):
+    """dX and dW (made if needed), their addresses, types and strides."""
+    dx = lddx = dw = lddw = 0
+    if dX is None and "dX" in need:
+        dX = _empty(X.shape[0], X.shape[1], X.dtype, X.device)
+    if dX is not None:
+        dx, lddx = _mat(dX, X.shape[0], X.shape[1], X.dtype, "dX")
+    if dW is None and "dW" in need:
+        dW = _empty_weights(W, layout, dw_dtype or X.dtype)
+    ddw = _DTYPES[X.dtype]
+    if dW is not None:
+        if dW.shape != W.shape:
+            raise ValueError("dW must be %d x %d" % tuple(W.shape))
+        dw, ddw, lddw = dW.data_ptr(), _dtype(dW, "dW"), _like_weights(dW, layout)
+    return dX, dx, lddx, dW, dw, ddw, lddw
 
 
 def _like_weights(dW, layout):
     """dW's row stride; it has to be stored as W is."""
-    if dW is None:
-        return 0
     K, N = dW.shape
     if K > 1 and N > 1:
         got, ld = _weights(dW, "dW")
