@@ -152,7 +152,8 @@ tsgemm_status_t make_config(tsffn_s* h, int kind, int64_t M, int64_t N, int64_t 
     }
     const bool pair = f.cfg.block_m == 256;
     f.kernel = kernel_of(kind, layout, f.cfg, out_kind(dout));
-    const int64_t need = tsg::smem_bytes_for(f.cfg.block_m, f.cfg.block_n, dout, f.cfg.stages, 1);
+    const int64_t need = tsg::smem_bytes_for(f.cfg.block_m, f.cfg.block_n, dout, f.cfg.stages, 1) +
+                         (kind == tsg::kEpiLinear ? static_cast<int64_t>(tsg::kResidBarBytes) : 0);
     if (!f.kernel || need > tsg::kSmemPerCtaMax) return TSGEMM_ERR_UNSUPPORTED;
     // (more than half the SM's shared memory, so one CTA owns each SM and
     // its tensor memory)
@@ -254,6 +255,16 @@ tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
     if (!ok_a || !ok_b || !ok_c) return TSGEMM_ERR_CUDA;
 
     tsg::FfnParams p{};
+    if (g.epi.saved) {
+        // (a linear layer's map ends with its columns; the copy engine may
+        // write the row's padding up to a 16-byte boundary)
+        bool ok = map(&p.saved[0], TSGEMM_F32, g.epi.saved, n_out, g.M, g.epi.lds, 32, 32, sw,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE);
+        if (gated)
+            ok = ok && map(&p.saved[1], TSGEMM_F32, g.epi.saved + n_out, n_out, g.M, g.epi.lds, 32, 32, sw,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE);
+        if (!ok) return TSGEMM_ERR_CUDA;
+    }
     p.M = static_cast<int32_t>(g.M);
     p.N = static_cast<int32_t>(n_out);
     p.K = static_cast<int32_t>(g.K);
@@ -276,6 +287,11 @@ tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
     p.status = h->status;
     p.timeout_ns = kTimeoutNs;
     p.epi = g.epi;
+
+    if (g.epi.residual && g.dout != TSGEMM_F32 &&
+        !map(&p.resid, g.dout, g.epi.residual, n_out, g.M, g.epi.ldr, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE))
+        return TSGEMM_ERR_CUDA;
 
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(static_cast<unsigned>(c.grid), 1, 1);

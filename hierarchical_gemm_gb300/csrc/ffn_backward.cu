@@ -57,10 +57,11 @@ __global__ void __launch_bounds__(256) linear_grad_sm103(const LinearGradArgs a,
                 float z[8];
                 load8_f32(a.saved + r * a.lds, col, a.N, z);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v, dv;
-                    act_both<kAct>(z[j], v, dv);
-                    d[j] *= dv;
+                for (int j = 0; j < 8; j += 2) {
+                    float2 v, dv;
+                    act_both<kAct>({z[j], z[j + 1]}, v, dv);
+                    d[j] *= dv.x;
+                    d[j + 1] *= dv.y;
                 }
             }
 #pragma unroll
@@ -114,11 +115,13 @@ __global__ void __launch_bounds__(256) gated_grad_sm103(const GatedGradArgs a) {
         load8_f32(z, col, a.F, g);
         load8_f32(z + a.F, col, a.F, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float v, dv;
-            act_both<kAct>(g[j], v, dv);
-            g[j] = d[j] * u[j] * dv;
-            u[j] = d[j] * v;
+        for (int j = 0; j < 8; j += 2) {
+            const float2 dh = {d[j], d[j + 1]};
+            float2 v, dv;
+            act_both<kAct>({g[j], g[j + 1]}, v, dv);
+            const float2 dg = mul2(mul2(dh, {u[j], u[j + 1]}), dv), du = mul2(dh, v);
+            g[j] = dg.x, g[j + 1] = dg.y;
+            u[j] = du.x, u[j + 1] = du.y;
         }
         uint16_t* out = static_cast<uint16_t*>(a.dGU) + r * 2 * a.F;
         store8_16<kBF16>(out, col, a.F, g);

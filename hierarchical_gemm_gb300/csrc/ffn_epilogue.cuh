@@ -21,62 +21,117 @@ namespace tsg {
 // The activations (the tsffn_act_t values).
 enum ActKind { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActSigmoid = 5 };
 
-// 1 / (1 + 2^-t), within a few fp32 ulps (ex2.approx, a fast division).
-// t -> -inf gives 1 / inf = 0, t -> inf gives 1.
-__device__ __forceinline__ float sigmoid_log2(float t) { return __fdividef(1.0f, 1.0f + ex2_approx(-t)); }
+// The activations work on pairs of values, for two reasons.  Multiplications
+// and additions of two fp32 values at once are one instruction each.  And the
+// approximate functions (ex2, rcp) run at an eighth of that rate, so the two
+// reciprocals a pair needs come from one: 1 / x = y / (x y).  With scalar
+// code the epilogue of a 4096 x 16384 x 4096 layer took up to a fifth of its
+// time (silu 621 thousand cycles, gelu by erfcf 800; none 565).
+
+// 1 / x by the hardware's approximation (within 1 ulp).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// (1 / x, 1 / y) for 1 <= x, y <= 2^63 or so: x y stays below fp32's limit.
+__device__ __forceinline__ float2 rcp_pair(float2 x) {
+    const float r = rcp_approx(x.x * x.y);
+    return {r * x.y, r * x.x};
+}
+__device__ __forceinline__ float2 splat(float x) { return {x, x}; }
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanhCubic = 0.044715f;                 // the tanh form's cubic coefficient
 constexpr float kTanhScale = 1.5957691216057308f;       // 2 sqrt(2 / pi)
-constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+// 1 / (1 + 2^-t), within a few fp32 ulps for t >= -63, and 0 below (where it
+// is under 1.1e-19; its product with t is too).  A NaN gives some number.
+__device__ __forceinline__ float2 sigmoid_log2(float2 t) {
+    const float2 e = {fminf(ex2_approx(-t.x), 0x1p63f), fminf(ex2_approx(-t.y), 0x1p63f)};
+    const float2 s = rcp_pair(add2(e, splat(1.0f)));
+    return {t.x < -63.0f ? 0.0f : s.x, t.y < -63.0f ? 0.0f : s.y};
+}
 
 // The tanh form of gelu is z sigma(2 sqrt(2 / pi) (z + 0.044715 z^3)), since
 // (1 + tanh u) / 2 = sigma(2 u): one exponential, no cancellation for z < 0.
-__device__ __forceinline__ float gelu_tanh_gate(float z) {
-    return sigmoid_log2(kTanhScale * kLog2e * z * fmaf(kTanhCubic * z, z, 1.0f));
+__device__ __forceinline__ float2 gelu_tanh_gate(float2 z) {
+    const float2 cubic = fma2(mul2(splat(kTanhScale * kLog2e * kTanhCubic), z), z, splat(kTanhScale * kLog2e));
+    return sigmoid_log2(mul2(z, cubic));
 }
-// gelu is z Phi(z) with Phi(z) = erfc(-z / sqrt 2) / 2, which keeps its
-// relative accuracy in the tail where 1 + erf cancels.
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-kSqrtHalf * z); }
+
+// gelu is z Phi(z), Phi the normal distribution function.  For |z|,
+//   1 - Phi(|z|) = erfc(|z| / sqrt 2) / 2 = exp(-z^2 / 2) t P(t),
+// t = 1 / (1 + 0.44 |z| / sqrt 2), P a polynomial of degree 7: the least
+// largest relative error of erfc(x) exp(x^2) / (2 t) over x in [0, 14]
+// (reweighted least squares on Chebyshev nodes; 1.9e-7).  In fp32 the result
+// keeps its relative accuracy in the tail, where 1 + erf cancels: within
+// 6e-7 for |z| < 2 and 8e-6 at |z| = 13, where the exponent's rounding is
+// what is left.  No branch, and the exponential is the one the derivative
+// needs too.
+__device__ __forceinline__ float2 normal_cdf(float2 z, float2& exp_half) {
+    const float2 q = mul2(mul2(z, z), splat(-0.5f * kLog2e));
+    exp_half = {ex2_approx(q.x), ex2_approx(q.y)};
+    const float2 size = {fminf(fabsf(z.x), 1e4f), fminf(fabsf(z.y), 1e4f)};  // (beyond, exp_half is 0)
+    const float2 t = rcp_pair(fma2(splat(0.311126977f), size, splat(1.0f)));
+    float2 s = fma2(splat(0.0357501954f), t, splat(-0.139577523f));
+    s = fma2(s, t, splat(0.149435446f));
+    s = fma2(s, t, splat(-0.0111487592f));
+    s = fma2(s, t, splat(0.108497605f));
+    s = fma2(s, t, splat(0.10846711f));
+    s = fma2(s, t, splat(0.124467745f));
+    s = fma2(s, t, splat(0.124108262f));
+    const float2 h = mul2(mul2(s, t), exp_half);
+    return {z.x < 0.0f ? h.x : 1.0f - h.x, z.y < 0.0f ? h.y : 1.0f - h.y};  // (a NaN stays one)
+}
 
 template <int kAct>
-__device__ __forceinline__ float act_value(float z) {
-    if constexpr (kAct == kActRelu) return z < 0.0f ? 0.0f : z;  // (a NaN stays one)
-    if constexpr (kAct == kActGelu) return z * normal_cdf(z);
-    if constexpr (kAct == kActGeluTanh) return z * gelu_tanh_gate(z);
-    if constexpr (kAct == kActSilu) return z * sigmoid_log2(kLog2e * z);
-    if constexpr (kAct == kActSigmoid) return sigmoid_log2(kLog2e * z);
+__device__ __forceinline__ float2 act_value(float2 z) {
+    if constexpr (kAct == kActRelu) return {z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y};  // (a NaN stays one)
+    if constexpr (kAct == kActGelu) {
+        float2 e;
+        return mul2(z, normal_cdf(z, e));
+    }
+    if constexpr (kAct == kActGeluTanh) return mul2(z, gelu_tanh_gate(z));
+    if constexpr (kAct == kActSilu) return mul2(z, sigmoid_log2(mul2(splat(kLog2e), z)));
+    if constexpr (kAct == kActSigmoid) {
+        const float2 s = sigmoid_log2(mul2(splat(kLog2e), z));
+        return {z.x == z.x ? s.x : z.x, z.y == z.y ? s.y : z.y};  // (a NaN stays one)
+    }
     return z;
 }
 
 // act(z) and act'(z).
 template <int kAct>
-__device__ __forceinline__ void act_both(float z, float& a, float& da) {
+__device__ __forceinline__ void act_both(float2 z, float2& a, float2& da) {
     if constexpr (kAct == kActRelu) {
-        a = z < 0.0f ? 0.0f : z;
-        da = z > 0.0f ? 1.0f : 0.0f;
+        a = act_value<kActRelu>(z);
+        da = {z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f};
     } else if constexpr (kAct == kActGelu) {
-        const float p = normal_cdf(z);
-        a = z * p;
-        da = fmaf(z * kInvSqrt2Pi, ex2_approx(-0.5f * kLog2e * z * z), p);
+        float2 e;
+        const float2 p = normal_cdf(z, e);
+        a = mul2(z, p);
+        da = fma2(mul2(z, splat(kInvSqrt2Pi)), e, p);
     } else if constexpr (kAct == kActGeluTanh) {
-        const float s = gelu_tanh_gate(z);
-        a = z * s;
+        const float2 s = gelu_tanh_gate(z);
+        a = mul2(z, s);
         // s (1 - s) is exactly 0 well before |z| = 16; the clamp keeps z^2
         // finite for the largest z, where 0 * inf would be NaN
-        const float c = fminf(fmaxf(z, -16.0f), 16.0f);
-        da = fmaf(c * s * (1.0f - s), kTanhScale * fmaf(3.0f * kTanhCubic * c, c, 1.0f), s);
+        const float2 c = {fminf(fmaxf(z.x, -16.0f), 16.0f), fminf(fmaxf(z.y, -16.0f), 16.0f)};
+        const float2 left = fma2(splat(-1.0f), mul2(s, s), s);  // s (1 - s)
+        const float2 slope = fma2(mul2(splat(3.0f * kTanhCubic * kTanhScale), c), c, splat(kTanhScale));
+        da = fma2(mul2(c, left), slope, s);
     } else if constexpr (kAct == kActSilu) {
-        const float s = sigmoid_log2(kLog2e * z);
-        a = z * s;
-        da = s * fmaf(z, 1.0f - s, 1.0f);
+        const float2 s = sigmoid_log2(mul2(splat(kLog2e), z));
+        a = mul2(z, s);
+        da = mul2(s, fma2(z, fma2(splat(-1.0f), s, splat(1.0f)), splat(1.0f)));
     } else if constexpr (kAct == kActSigmoid) {
-        a = sigmoid_log2(kLog2e * z);
-        da = a * (1.0f - a);
+        a = act_value<kActSigmoid>(z);
+        da = fma2(splat(-1.0f), mul2(a, a), a);
     } else {
         a = z;
-        da = 1.0f;
+        da = splat(1.0f);
     }
 }
 
@@ -165,67 +220,67 @@ __device__ __forceinline__ void load8(int kind, const void* p, int64_t i, int64_
 
 // --------------------------------------------------------- the epilogue --
 
-// Lane's row `row`, columns [col, col + 32) of the fp32 sums in r: writes
-// them to the saved pre-activations at column `at` (the linear layer's own
-// column, or F later for the up half).  Rows of the saved array are 8
-// floats' multiples long, so a group of four that starts inside a row's n
-// columns stays inside the row.
-__device__ __forceinline__ void save_preact(const FfnEpilogue& e, int row, int M, int col, int n, int64_t at,
-                                            const uint32_t (&r)[32]) {
-    if (row >= M) return;
-    float* dst = e.saved + static_cast<int64_t>(row) * e.lds + at;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (col + 4 * j < n) st_global_v4(dst + 4 * j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-}
-
-// The linear layer's epilogue on 32 columns of one row: + bias, saved
-// pre-activation, activation, + residual (kResid: its ElemKind).
+// + 32 columns of one row of the residual, read from memory (kResid: its
+// ElemKind).
 template <int kResid>
-__device__ __forceinline__ void linear_epilogue(const FfnEpilogue& e, int row, int M, int col, int n,
-                                                uint32_t (&r)[32]) {
-    if (e.bias_kind != kElemNone) {
+__device__ __forceinline__ void add_residual(const FfnEpilogue& e, int row, int M, int col, int n, uint32_t (&r)[32]) {
+    if (!e.residual || row >= M) return;
+    constexpr int64_t kBytes = kResid == kElemF32 ? 4 : 2;
+    const char* p = static_cast<const char*>(e.residual) + static_cast<int64_t>(row) * e.ldr * kBytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float b[8];
-            load8(e.bias_kind, e.bias, col + 8 * j, n, b);
+    for (int j = 0; j < 4; ++j) {
+        float v[8];
+        load8(kResid, p, col + 8 * j, n, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[8 * j + i] = __float_as_uint(__uint_as_float(r[8 * j + i]) + b[i]);
-        }
+        for (int i = 0; i < 8; ++i) r[8 * j + i] = __float_as_uint(__uint_as_float(r[8 * j + i]) + v[i]);
     }
-    if (e.saved) save_preact(e, row, M, col, n, col, r);
-    if (e.act != kActNone) {
-        with_act(e.act, [&](auto a) {
+}
+// r + 8 packed 16-bit values.
+template <bool kBF16>
+__device__ __forceinline__ void add_packed8(uint4 w, uint32_t* r) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                r[i] = __float_as_uint(act_value<decltype(a)::value>(__uint_as_float(r[i])));
-        });
-    }
-    if (e.residual && row < M) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float b[8];
-            constexpr int64_t kBytes = kResid == kElemF32 ? 4 : 2;
-            load8(kResid, static_cast<const char*>(e.residual) + static_cast<int64_t>(row) * e.ldr * kBytes,
-                  col + 8 * j, n, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[8 * j + i] = __float_as_uint(__uint_as_float(r[8 * j + i]) + b[i]);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<kBF16>(x[i]);
+        r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) + f.x);
+        r[2 * i + 1] = __float_as_uint(__uint_as_float(r[2 * i + 1]) + f.y);
     }
 }
 
-// The gated layer's on 32 columns: g (gate sums) becomes act(g) * u.
-__device__ __forceinline__ void gated_epilogue(const FfnEpilogue& e, int row, int M, int col, int F,
-                                               uint32_t (&g)[32], const uint32_t (&u)[32]) {
-    if (e.saved) {
-        save_preact(e, row, M, col, F, col, g);
-        save_preact(e, row, M, col, F, static_cast<int64_t>(F) + col, u);
-    }
-    with_act(e.act, [&](auto a) {
+// This lane's value of the bias of columns [col, col + 32): asked for a chunk
+// ahead, and handed round by shuffles when the sums are there.  (Every lane
+// reading all 32 values when it needs them costs the L2 latency a chunk:
+// 637 thousand cycles against 565 for 4096 x 16384 x 4096 in 256 x 512 tiles.)
+__device__ __forceinline__ float lane_bias(const FfnEpilogue& e, int col, int n, int lane) {
+    const int c = col + lane;
+    if (e.bias_kind == kElemNone || c >= n) return 0.0f;
+    return e.bias_kind == kElemBF16 ? load16<true>(e.bias, c)
+                                    : (e.bias_kind == kElemF16 ? load16<false>(e.bias, c)
+                                                               : static_cast<const float*>(e.bias)[c]);
+}
+__device__ __forceinline__ void add_bias(const FfnEpilogue& e, float mine, uint32_t (&r)[32]) {
+    if (e.bias_kind == kElemNone) return;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            g[i] = __float_as_uint(act_value<decltype(a)::value>(__uint_as_float(g[i])) * __uint_as_float(u[i]));
-    });
+    for (int i = 0; i < 32; ++i)
+        r[i] = __float_as_uint(__uint_as_float(r[i]) + __shfl_sync(0xffffffffu, mine, i));
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t* r) { return {__uint_as_float(r[0]), __uint_as_float(r[1])}; }
+__device__ __forceinline__ void set_pair(uint32_t* r, float2 v) {
+    r[0] = __float_as_uint(v.x);
+    r[1] = __float_as_uint(v.y);
+}
+template <int kAct>
+__device__ __forceinline__ void activate(uint32_t (&r)[32]) {
+    if constexpr (kAct != kActNone) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) set_pair(r + i, act_value<kAct>(pair_of(r + i)));
+    }
+}
+// g (gate sums) becomes act(g) * u.
+template <int kAct>
+__device__ __forceinline__ void gate(uint32_t (&g)[32], const uint32_t (&u)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) set_pair(g + i, mul2(act_value<kAct>(pair_of(g + i)), pair_of(u + i)));
 }
 
 }  // namespace tsg

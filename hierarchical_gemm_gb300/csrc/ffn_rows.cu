@@ -58,12 +58,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
-                 : "memory");
-    return v;
-}
 // Bytes of the 8 values from i on that are below n: 0 to 16.
 __device__ __forceinline__ int bytes_in(int64_t i, int64_t n) {
     const int64_t left = n - i;
@@ -220,9 +214,9 @@ __global__ void __launch_bounds__(32 * kWarps, (RowsShape<kRCR, MT>::kPerSM)) fe
             const uint32_t src = ring_rd + slot * S::kStepBytes, srcx = ring_rdx + slot * S::kStepBytes;
             uint4 w[S::kWVecs], x[MT];
 #pragma unroll
-            for (int v = 0; v < S::kWVecs; ++v) w[v] = ld_shared_u4(src + v * 512u);
+            for (int v = 0; v < S::kWVecs; ++v) w[v] = ld_shared_v4(src + v * 512u);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) x[i] = ld_shared_u4(srcx + (S::kWVecs + i) * 512u);
+            for (int i = 0; i < MT; ++i) x[i] = ld_shared_v4(srcx + (S::kWVecs + i) * 512u);
             if constexpr (kRCR) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -310,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWarps, (RowsShape<kRCR, MT>::kPerSM)) fe
                     e.saved[m * e.lds + col] = z;
                     e.saved[m * e.lds + a.N + col] = u;
                 }
-                with_act(e.act, [&](auto act) { v = act_value<decltype(act)::value>(z); });
+                with_act(e.act, [&](auto act) { v = act_value<decltype(act)::value>(splat(z)).x; });
                 v *= u;
             } else {
                 if (e.bias_kind == kElemF32)
@@ -318,7 +312,7 @@ __global__ void __launch_bounds__(32 * kWarps, (RowsShape<kRCR, MT>::kPerSM)) fe
                 else if (e.bias_kind != kElemNone)
                     z += load16<kBF16>(e.bias, col);
                 if (e.saved) e.saved[m * e.lds + col] = z;
-                with_act(e.act, [&](auto act) { v = act_value<decltype(act)::value>(z); });
+                with_act(e.act, [&](auto act) { v = act_value<decltype(act)::value>(splat(z)).x; });
                 if (e.residual)
                     v += a.out_f32 ? static_cast<const float*>(e.residual)[m * e.ldr + col]
                                    : load16<kBF16>(e.residual, m * e.ldr + col);

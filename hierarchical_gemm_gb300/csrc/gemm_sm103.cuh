@@ -111,7 +111,14 @@ struct GemmParams {
 enum EpiKind { kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2 };
 struct FfnParams : GemmParams {
     FfnEpilogue epi;
+    // the saved pre-activations as 32 x 32 fp32 boxes in the 128-byte
+    // swizzle: the linear layer's, or the gate and the up half's
+    CUtensorMap saved[2];
+    CUtensorMap resid;  // 16-bit residuals, as C's map
 };
+// Barriers of the residual's copies: two per epilogue warp.
+constexpr uint32_t kResidBarBytes = 2u * 8u * kEpiWarps;
+constexpr int elem_of(int out) { return out == kOutF32 ? kElemF32 : (out == kOutBF16 ? kElemBF16 : kElemF16); }
 template <int kEpi>
 using ParamsFor = std::conditional_t<kEpi == kEpiPlain, GemmParams, FfnParams>;
 
@@ -259,14 +266,129 @@ struct CStager {
     uint32_t which;  // buffer to fill next
     int lane;
 
+    // A linear layer's 16-bit residual is copied, block by block, into the
+    // staging buffer that its output will leave from (each lane adds its own
+    // row and writes it back), asked for before the sums are: `pending` is set
+    // while the copy for buffer `which` is under way.
+    static constexpr bool kResidCopy = kEpi == kEpiLinear && kOut != kOutF32;
+    uint32_t rbar = 0;    // this warp's two barriers
+    uint32_t rphase = 0;  // and their phases
+    bool pending = false;
+    float bias = 0.0f;    // this lane's bias of the next chunk
+
+    // Whether the block at (row0, col0) has a residual to copy: one that
+    // holds a row end inside a 16-byte piece goes value by value.
+    __device__ __forceinline__ bool resid_block(const ParamsFor<kEpi>& p, int row0, int col0) const {
+        if constexpr (kResidCopy)
+            return p.epi.residual && row0 < p.M && col0 < p.N && ((p.N & 7) == 0 || col0 + 32 <= p.N);
+        else
+            return false;
+    }
+    __device__ __forceinline__ void request(const ParamsFor<kEpi>& p, int row0, int col0) {
+        if constexpr (kResidCopy) {
+            if (!resid_block(p, row0, col0)) return;
+            if (lane == 0) {
+                bulk_wait_group_read<1>();  // the store that used this buffer last has read it
+                mbar_arrive_expect_tx(rbar + 8 * which, epi_buf_bytes<kOut>());
+                tma_load_2d(buf0 + which * epi_buf_bytes<kOut>(), &p.resid, rbar + 8 * which, col0, row0);
+            }
+            pending = true;
+        }
+    }
+    // Wait for the pending copy: also when the CTA is giving up, since the
+    // copy has to land before the buffer is used again or the CTA leaves.
+    __device__ __forceinline__ void await(const WaitCtl& ctl) {
+        wait_bounded(rbar + 8 * which, (rphase >> which) & 1u, ctl, false);
+        rphase ^= 1u << which;
+        pending = false;
+    }
+
     // The finished sums of this lane's row, columns [col0, col0 + 32): a
     // linear layer's epilogue comes first.
     __device__ __forceinline__ void put(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, int row0, int col0,
-                                        uint32_t (&r)[32]) {
-        if constexpr (kEpi == kEpiLinear)
-            linear_epilogue<kOut == kOutF32 ? kElemF32 : (kOut == kOutBF16 ? kElemBF16 : kElemF16)>(
-                p.epi, row0 + lane, p.M, col0, p.N, r);
+                                        uint32_t (&r)[32], const WaitCtl& ctl) {
+        if constexpr (kEpi == kEpiLinear) {
+            if (!p.epi.saved) request(p, row0, col0);
+            bias = lane_bias(p.epi, col0, p.N, lane);
+            with_act(p.epi.act, [&](auto a) { finish<decltype(a)::value>(p, tmC, row0, col0, -1, r, ctl); });
+        } else {
+            store(p, tmC, row0, col0, r);
+        }
+    }
+    // The linear layer's epilogue, its bias and its residual's copy asked for
+    // before.  (With saved pre-activations, which leave through the same
+    // buffers, the copy is asked for once they have.)  `next`: the column
+    // whose bias comes after this one's, or -1.
+    template <int kAct>
+    __device__ __forceinline__ void finish(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, int row0, int col0, int next,
+                                           uint32_t (&r)[32], const WaitCtl& ctl) {
+        add_bias(p.epi, bias, r);
+        if (next >= 0) bias = lane_bias(p.epi, next, p.N, lane);
+        if (p.epi.saved) {
+            save(&p.saved[0], p.epi.saved + col0, p.epi.lds, row0, col0, p.M, p.N, r);
+            request(p, row0, col0);
+        }
+        activate<kAct>(r);
+        if constexpr (kResidCopy) {
+            if (pending) {
+                await(ctl);
+                const uint32_t row = buf0 + which * epi_buf_bytes<kOut>() + lane * 64;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    add_packed8<kOut == kOutBF16>(ld_shared_v4(row + ((j ^ ((lane >> 1) & 3)) << 4)), r + 8 * j);
+            } else if (p.epi.residual) {
+                add_residual<elem_of(kOut)>(p.epi, row0 + lane, p.M, col0, p.N, r);
+            }
+        } else {
+            add_residual<elem_of(kOut)>(p.epi, row0 + lane, p.M, col0, p.N, r);
+        }
         store(p, tmC, row0, col0, r);
+    }
+
+    // The gated layer's: g and u are the sums of 32 columns of H.
+    template <int kAct>
+    __device__ __forceinline__ void finish_gated(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, int row0, int col0,
+                                                 uint32_t (&g)[32], const uint32_t (&u)[32]) {
+        if (p.epi.saved) {
+            save(&p.saved[0], p.epi.saved + col0, p.epi.lds, row0, col0, p.M, p.N, g);
+            save(&p.saved[1], p.epi.saved + p.N + col0, p.epi.lds, row0, col0, p.M, p.N, u);
+        }
+        gate<kAct>(g, u);
+        store(p, tmC, row0, col0, g);
+    }
+
+    // Write 32 fp32 pre-activations of this lane's row, columns [col0, col0 +
+    // 32) of n.  16-bit outputs: through both staging buffers as one 32 x 32
+    // fp32 block and a tiled store (whole lines, clipped at the edges), after
+    // which the buffers are free again.  Without staging (fp32 outputs): from
+    // registers; rows of the saved array are multiples of 8 floats, so a group
+    // of four that starts inside a row's n columns stays inside the row.
+    __device__ __forceinline__ void save(const CUtensorMap* tm, float* dst, int64_t ld, int row0, int col0, int M, int n,
+                                         const uint32_t (&r)[32]) {
+        if constexpr (kOut == kOutF32) {
+            if (row0 + lane >= M) return;
+            float* d = dst + static_cast<int64_t>(row0 + lane) * ld;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col0 + 4 * j < n) st_global_v4(d + 4 * j, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        } else {
+            if (lane == 0) bulk_wait_group_read<0>();  // earlier stores have read both buffers
+            __syncwarp();
+            // 128-byte rows in the 128-byte swizzle: chunk j of row l sits at
+            // chunk position j ^ (l mod 8)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                st_shared_v4(buf0 + lane * 128 + ((j ^ (lane & 7)) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2],
+                             r[4 * j + 3]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                if (row0 < M && col0 < n) tma_store_2d(tm, buf0, col0, row0);
+                bulk_commit_group();
+                bulk_wait_group_read<0>();
+            }
+            __syncwarp();
+        }
     }
 
     // Convert 32 fp32 values (this lane's row, 32 consecutive columns) and
@@ -343,7 +465,10 @@ struct CStager {
     // All of this warp's stores have read their staging buffers, so the
     // CTA may leave: the writes to C complete on their own, before the
     // grid is done (nothing in the kernel reads C back).
-    __device__ __forceinline__ void drain() {
+    __device__ __forceinline__ void drain([[maybe_unused]] const WaitCtl& ctl) {
+        if constexpr (kResidCopy) {
+            if (pending) await(ctl);  // (of a unit given up)
+        }
         if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
     }
@@ -416,7 +541,7 @@ __device__ __forceinline__ void prefetch_sk_partials(const GemmParams& p, const 
 template <int BN, int kOut, int kEpi, class Release>
 __device__ __forceinline__ void drain_parts(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, CStager<kOut, kEpi>& out,
                                             const Unit& un, uint32_t tbase, int row0, int row_local, int64_t h,
-                                            const EpiAux& aux, int c_begin, Release&& release) {
+                                            const EpiAux& aux, int c_begin, const WaitCtl& ctl, Release&& release) {
     const int n = un.nsplit, me = un.split;
     const int q = row_local >> 5, lane = row_local & 31;
     const int col0 = un.tn * BN;
@@ -494,7 +619,7 @@ __device__ __forceinline__ void drain_parts(const ParamsFor<kEpi>& p, const CUte
         uint32_t w[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(acc[j]);
-        out.put(p, tmC, row0, col0 + c, w);
+        out.put(p, tmC, row0, col0 + c, w, ctl);
         if (lane == 0) *reinterpret_cast<volatile int*>(cnt) = 0;  // ready for the next launch
     }
 }
@@ -509,16 +634,18 @@ __device__ __forceinline__ void drain_gated(const FfnParams& p, const CUtensorMa
     static_assert(BN % 128 == 0, "each warpgroup drains whole 32-column chunks of both halves");
     const int col0 = un.tn * (BN / 2);
     const int c_end = c_begin + BN / 4;
+    // (the activation is chosen outside the loop: see drain_unit)
+    with_act(p.epi.act, [&](auto act) {
 #pragma unroll 1
-    for (int c = c_begin; c < c_end; c += 32) {
-        uint32_t g[32], u[32];
-        tmem_ld_32x32b_x32(tbase + c, g);
-        tmem_ld_32x32b_x32(tbase + c + BN / 2, u);
-        tmem_ld_wait();
-        if (c + 32 >= c_end) release();  // this thread's accumulator part is in registers
-        gated_epilogue(p.epi, row0 + out.lane, p.M, col0 + c, p.N, g, u);
-        out.store(p, tmC, row0, col0 + c, g);
-    }
+        for (int c = c_begin; c < c_end; c += 32) {
+            uint32_t g[32], u[32];
+            tmem_ld_32x32b_x32(tbase + c, g);
+            tmem_ld_32x32b_x32(tbase + c + BN / 2, u);
+            tmem_ld_wait();
+            if (c + 32 >= c_end) release();  // this thread's accumulator part is in registers
+            out.template finish_gated<decltype(act)::value>(p, tmC, row0, col0 + c, g, u);
+        }
+    });
 }
 
 // r becomes 0 + p_0 + ... + p_{n-1} of one 32-column chunk, this part's own
@@ -625,8 +752,9 @@ __device__ __forceinline__ void drain_gated_parts(const FfnParams& p, const CUte
         tmem_ld_wait();
         sum_parts<BN>(p, un, aux, h, up, q, lane, u);
         if (lane == 0) *reinterpret_cast<volatile int*>(cnt) = 0;  // ready for the next launch
-        gated_epilogue(p.epi, row0 + lane, p.M, col0 + c, p.N, g, u);
-        out.store(p, tmC, row0, col0 + c, g);
+        with_act(p.epi.act, [&](auto act) {
+            out.template finish_gated<decltype(act)::value>(p, tmC, row0, col0 + c, g, u);
+        });
     }
     release();
 }
@@ -634,7 +762,7 @@ __device__ __forceinline__ void drain_gated_parts(const FfnParams& p, const CUte
 template <int BN, int kOut, int kEpi, class Release>
 __device__ __forceinline__ void drain_unit(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, CStager<kOut, kEpi>& out,
                                            const Unit& un, uint32_t tbase, int row0, int row_local, int64_t h,
-                                           const EpiAux& aux, int c_begin, Release&& release) {
+                                           const EpiAux& aux, int c_begin, const WaitCtl& ctl, Release&& release) {
     if constexpr (kEpi == kEpiGated) {
         if (un.nsplit > 1)
             drain_gated_parts<BN, kOut>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);
@@ -642,19 +770,56 @@ __device__ __forceinline__ void drain_unit(const ParamsFor<kEpi>& p, const CUten
             drain_gated<BN, kOut>(p, tmC, out, un, tbase, row0, c_begin, release);
     } else {
         if (un.nsplit > 1) {
-            drain_parts<BN, kOut, kEpi>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, release);
+            drain_parts<BN, kOut, kEpi>(p, tmC, out, un, tbase, row0, row_local, h, aux, c_begin, ctl, release);
             return;
         }
         const int col0 = un.tn * BN;
         const int c_end = c_begin + BN / 2;  // this warpgroup's half of the columns
+        if constexpr (kEpi == kEpiLinear) {
+            // The activation is chosen outside the loop: jumping to one of
+            // them and back for every chunk costs a few hundred cycles each
+            // time, instruction fetches mostly (relu, with its 64
+            // instructions, cost 380 a chunk).
+            with_act(p.epi.act, [&](auto act) {
 #pragma unroll 1
-        for (int c = c_begin; c < c_end; c += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tbase + c, r);
-            tmem_ld_wait();
-            if (c + 32 >= c_end) release();  // this thread's accumulator part is in registers
-            out.put(p, tmC, row0, col0 + c, r);
+                for (int c = c_begin; c < c_end; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tbase + c, r);
+                    tmem_ld_wait();
+                    const bool more = c + 32 < c_end;
+                    if (!more) release();  // this thread's accumulator part is in registers
+                    out.template finish<decltype(act)::value>(p, tmC, row0, col0 + c, more ? col0 + c + 32 : -1, r, ctl);
+                    if (!p.epi.saved && more) out.request(p, row0, col0 + c + 32);
+                }
+            });
+        } else {
+#pragma unroll 1
+            for (int c = c_begin; c < c_end; c += 32) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tbase + c, r);
+                tmem_ld_wait();
+                if (c + 32 >= c_end) release();  // this thread's accumulator part is in registers
+                out.put(p, tmC, row0, col0 + c, r, ctl);
+            }
         }
+    }
+}
+
+// Before a linear unit's sums are ready: its first chunk's bias, and its
+// residual on the way, into L2, and the first block of a whole tile into its
+// buffer.
+template <int BN, int kOut>
+__device__ __forceinline__ void ask_operands(const FfnParams& p, CStager<kOut, kEpiLinear>& out, const Unit& un, int row0,
+                                             int c_begin) {
+    const int col0 = un.tn * BN + c_begin;
+    out.bias = lane_bias(p.epi, col0, p.N, out.lane);
+    if constexpr (CStager<kOut, kEpiLinear>::kResidCopy) {
+        if (!p.epi.residual) return;
+        const bool now = un.nsplit == 1 && !p.epi.saved;
+        if (now) out.request(p, row0, col0);
+        if (out.lane == 0)
+            for (int c = now ? 32 : 0; c < BN / 2; c += 32)
+                if (row0 < p.M && col0 + c < p.N) tma_prefetch_2d(&p.resid, col0 + c, row0);
     }
 }
 
@@ -798,7 +963,7 @@ __device__ __forceinline__ bool drain_cs(const GemmParams& p, const CUtensorMap*
         } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(acc[j]);
-            out.put(p, tmC, row0, col0 + c, r);
+            out.put(p, tmC, row0, col0 + c, r, ctl);
         }
         phase ^= 1u;
     }
@@ -812,7 +977,7 @@ __device__ __forceinline__ bool drain_cs(const GemmParams& p, const CUtensorMap*
 template <int BN, int kOut, int kLayout, bool kF8 = false, bool kCS = false, int kEpi = kEpiPlain>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_sm103_1sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const ParamsFor<kEpi> p) {
+                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ ParamsFor<kEpi> p) {
     using TS = TileShape<BN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -846,6 +1011,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(tempty_bar(a), kEpiThreads);
         }
         mbar_init(drain_bar, 1);
+        if constexpr (CStager<kOut, kEpi>::kResidCopy) {
+            for (int w = 0; w < 2 * kEpiWarps; ++w) mbar_init(bars + 8u * (2 * S + 5) + 16u + 8u * w, 1);
+        }
         if constexpr (kCS) {
             for (int w = 0; w < 4; ++w) mbar_init(cs_bars + 8u * w, 128);  // every lane of a warpgroup
         }
@@ -984,6 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int etid = threadIdx.x - 64;   // 0..255
         const int row_local = q * 32 + lane;
         CStager<kOut, kEpi> out{epi_smem + static_cast<uint32_t>(e) * 2u * epi_buf_bytes<kOut>(), 0u, lane};
+        out.rbar = bars + 8u * (2 * S + 5) + 16u + 16u * static_cast<uint32_t>(e);
         int acc = 0;
         uint32_t acc_phase = 0;
         const EpiAux aux{static_cast<int64_t>(blockIdx.x), 1};
@@ -995,13 +1164,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!next_unit(j, un)) break;
             const int tm = un.tm;
             prefetch_sk_partials<BN>(p, un, aux, etid);
+            const int row0 = tm * kBM + q * 32;
+            if constexpr (kEpi == kEpiLinear) ask_operands<BN, kOut>(p, out, un, row0, c_begin);
             int ok = 1;
             if (lane == 0) ok = wait_bounded(tfull_bar(acc), acc_phase, ctl) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             __syncwarp();
             tc_fence_after();
-            const int row0 = tm * kBM + q * 32;
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TS::kAccCols;
             auto release = [&]() {
                 tc_fence_before();
@@ -1012,14 +1182,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         cs_bars + 8u * wg, cs_bars + 8u * (2 + wg), cs_phase, ctl, release))
                     break;
             } else {
-                drain_unit<BN, kOut, kEpi>(p, &tmC, out, un, tbase, row0, row_local, un.slot, aux, c_begin, release);
+                drain_unit<BN, kOut, kEpi>(p, &tmC, out, un, tbase, row0, row_local, un.slot, aux, c_begin, ctl,
+                                           release);
             }
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
         }
-        out.drain();  // this warp's output stores have read shared memory
+        out.drain(ctl);  // this warp's output stores have read shared memory
     }
 
     // ------------------------------------------------------------ exit --

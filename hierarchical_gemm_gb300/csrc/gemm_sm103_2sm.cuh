@@ -54,7 +54,7 @@ __host__ __device__ constexpr uint32_t smem_bytes_2sm(int stages) {
 template <int BN, int kOut, int kLayout, bool kF8 = false, int kEpi = kEpiPlain>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_sm103_2sm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const ParamsFor<kEpi> p) {
+                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ ParamsFor<kEpi> p) {
     using PS = PairShape<BN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -90,6 +90,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(tempty_bar(a), PS::kWide ? kEpiWarps : 2 * kEpiWarps);
         }
         mbar_init(drain_bar, 1);
+        if constexpr (CStager<kOut, kEpi>::kResidCopy) {
+            for (int w = 0; w < 2 * kEpiWarps; ++w) mbar_init(bars + 8u * (2 * S + 5) + 16u + 8u * w, 1);
+        }
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tmap(&tmA);
@@ -241,6 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int etid = threadIdx.x - 64;
         const int row_local = q * 32 + lane;
         CStager<kOut, kEpi> out{epi_smem + static_cast<uint32_t>(e) * 2u * epi_buf_bytes<kOut>(), 0u, lane};
+        out.rbar = bars + 8u * (2 * S + 5) + 16u + 16u * static_cast<uint32_t>(e);
         int acc = 0;
         uint32_t acc_phase = 0;
         // Release accumulator `a` to the leader's MMA issuer.
@@ -260,13 +264,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!unit_at(p, cluster_id, nclusters, j, un)) break;
             const int tm = un.tm;
             prefetch_sk_partials<BN>(p, un, aux, etid);
+            const int row0 = tm * (2 * kBM) + static_cast<int>(half) * kBM + q * 32;
+            if constexpr (kEpi == kEpiLinear) ask_operands<BN, kOut>(p, out, un, row0, c_begin);
             int ok = 1;
             if (lane == 0) ok = wait_bounded(tfull_bar(acc), acc_phase, ctl) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             __syncwarp();
             tc_fence_after();
-            const int row0 = tm * (2 * kBM) + static_cast<int>(half) * kBM + q * 32;
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * PS::kAccCols;
             // workspace tile and counter of this CTA's 128-row half
             const int64_t wh = un.slot * 2 + half;
@@ -275,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // of the same numbers; gated: every warp reads both accumulators,
             // and the issuer waits for both releases)
             const int a_now = PS::kWide ? (e >> 2) : acc;
-            drain_unit<BN, kOut, kEpi>(p, &tmC, out, un, tbase, row0, row_local, wh, aux, c_begin,
+            drain_unit<BN, kOut, kEpi>(p, &tmC, out, un, tbase, row0, row_local, wh, aux, c_begin, ctl,
                                  [&]() { release_acc(a_now); });
             if (PS::kWide) {
                 acc_phase ^= 1u;
@@ -284,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 acc_phase ^= 1u;
             }
         }
-        out.drain();  // this warp's output stores have read shared memory
+        out.drain(ctl);  // this warp's output stores have read shared memory
     }
 
     // ------------------------------------------------------------ exit --
