@@ -298,6 +298,9 @@ tsgemm_status_t run_product(tsffn_s* h, const Product& g, cudaStream_t stream) {
     lc.blockDim = dim3(tsg::kThreads, 1, 1);
     lc.dynamicSmemBytes = static_cast<size_t>(f.smem);
     lc.stream = stream;
+    cudaLaunchAttribute attr = tsg::dependent_launch();
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
     // (a plain kernel takes the GemmParams that FfnParams begins with)
     void* args[4] = {&tmA, &tmB, &tmC, &p};
     if (cudaLaunchKernelExC(&lc, f.kernel, args) != cudaSuccess) {

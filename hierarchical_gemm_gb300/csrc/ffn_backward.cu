@@ -48,6 +48,8 @@ __global__ void __launch_bounds__(256) linear_grad_sm103(const LinearGradArgs a,
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kStripCols + tx * 8;
     const int64_t r1 = chunk_begin(a.M, blockIdx.y + 1, gridDim.y);
+    griddep_launch();
+    griddep_wait();
     float acc[8] = {};
     if (col < a.N) {
         for (int64_t r = chunk_begin(a.M, blockIdx.y, gridDim.y) + ty; r < r1; r += kRowLanes) {
@@ -106,7 +108,9 @@ template <bool kBF16, int kAct>
 __global__ void __launch_bounds__(256) gated_grad_sm103(const GatedGradArgs a) {
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kStripCols + tx * 8;
+    griddep_launch();
     if (col >= a.F) return;
+    griddep_wait();
     const int64_t r1 = chunk_begin(a.M, blockIdx.y + 1, gridDim.y);
     for (int64_t r = chunk_begin(a.M, blockIdx.y, gridDim.y) + ty; r < r1; r += kRowLanes) {
         float d[8], g[8], u[8];
@@ -129,25 +133,32 @@ __global__ void __launch_bounds__(256) gated_grad_sm103(const GatedGradArgs a) {
     }
 }
 
+// Calls launch(bf16, activation) with both as compile-time values.
 template <class Launch>
 cudaError_t by_act(bool bf16, int act, Launch&& launch) {
     auto with = [&](auto b) {
-        constexpr bool B = decltype(b)::value;
         switch (act) {
-            case kActRelu: launch(b, std::integral_constant<int, kActRelu>{}); break;
-            case kActGelu: launch(b, std::integral_constant<int, kActGelu>{}); break;
-            case kActGeluTanh: launch(b, std::integral_constant<int, kActGeluTanh>{}); break;
-            case kActSilu: launch(b, std::integral_constant<int, kActSilu>{}); break;
-            case kActSigmoid: launch(b, std::integral_constant<int, kActSigmoid>{}); break;
-            default: launch(b, std::integral_constant<int, kActNone>{}); break;
+            case kActRelu: return launch(b, std::integral_constant<int, kActRelu>{});
+            case kActGelu: return launch(b, std::integral_constant<int, kActGelu>{});
+            case kActGeluTanh: return launch(b, std::integral_constant<int, kActGeluTanh>{});
+            case kActSilu: return launch(b, std::integral_constant<int, kActSilu>{});
+            case kActSigmoid: return launch(b, std::integral_constant<int, kActSigmoid>{});
+            default: return launch(b, std::integral_constant<int, kActNone>{});
         }
-        (void)B;
     };
-    if (bf16)
-        with(std::true_type{});
-    else
-        with(std::false_type{});
-    return cudaGetLastError();
+    return bf16 ? with(std::true_type{}) : with(std::false_type{});
+}
+
+template <class... Args>
+cudaError_t launch_grid(void (*kernel)(Args...), int64_t strips, int64_t chunks, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(chunks), 1);
+    lc.blockDim = dim3(256, 1, 1);
+    lc.stream = stream;
+    cudaLaunchAttribute attr = dependent_launch();
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, args...);
 }
 
 // Row chunks: enough blocks for 8 per SM, at least 32 rows a chunk.
@@ -169,8 +180,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const ColumnSums& sums, 
         if (strips > sums.num_counters || y < 1) y = 1;
     }
     return by_act(a.bf16, a.act, [&](auto b, auto act) {
-        linear_grad_sm103<decltype(b)::value, decltype(act)::value>
-            <<<dim3(static_cast<unsigned>(strips), static_cast<unsigned>(y)), 256, 0, stream>>>(a, sums);
+        return launch_grid(&linear_grad_sm103<decltype(b)::value, decltype(act)::value>, strips, y, stream, a, sums);
     });
 }
 
@@ -178,8 +188,7 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, int num_sms, cudaStream_t 
     const int64_t strips = (a.F + kStripCols - 1) / kStripCols;
     const int64_t y = row_chunks(a.M, strips, num_sms);
     return by_act(a.bf16, a.act, [&](auto b, auto act) {
-        gated_grad_sm103<decltype(b)::value, decltype(act)::value>
-            <<<dim3(static_cast<unsigned>(strips), static_cast<unsigned>(y)), 256, 0, stream>>>(a);
+        return launch_grid(&gated_grad_sm103<decltype(b)::value, decltype(act)::value>, strips, y, stream, a);
     });
 }
 

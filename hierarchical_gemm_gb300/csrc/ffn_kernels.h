@@ -9,6 +9,16 @@
 
 namespace tsg {
 
+// The launch attribute of a programmatic dependent (see griddep_wait): a
+// kernel of a chain sets up while the one before it drains, 1 to 2 us a
+// launch.
+inline cudaLaunchAttribute dependent_launch() {
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 // Types of a vector that a kernel learns when it runs.
 enum ElemKind { kElemNone = 0, kElemF16 = 1, kElemBF16 = 2, kElemF32 = 3 };
 

@@ -303,13 +303,17 @@ struct CStager {
         pending = false;
     }
 
+    // Ask for the operands of a linear layer's chunk.
+    __device__ __forceinline__ void ask(const ParamsFor<kEpi>& p, int row0, int col0) {
+        if (!p.epi.saved) request(p, row0, col0);
+        bias = lane_bias(p.epi, col0, p.N, lane);
+    }
+
     // The finished sums of this lane's row, columns [col0, col0 + 32): a
-    // linear layer's epilogue comes first.
+    // linear layer's epilogue comes first (its operands have been asked for).
     __device__ __forceinline__ void put(const ParamsFor<kEpi>& p, const CUtensorMap* tmC, int row0, int col0,
                                         uint32_t (&r)[32], const WaitCtl& ctl) {
         if constexpr (kEpi == kEpiLinear) {
-            if (!p.epi.saved) request(p, row0, col0);
-            bias = lane_bias(p.epi, col0, p.N, lane);
             with_act(p.epi.act, [&](auto a) { finish<decltype(a)::value>(p, tmC, row0, col0, -1, r, ctl); });
         } else {
             store(p, tmC, row0, col0, r);
@@ -574,6 +578,8 @@ __device__ __forceinline__ void drain_parts(const ParamsFor<kEpi>& p, const CUte
             last = __shfl_sync(0xffffffffu, last, 0);
             if (!last) continue;
         }
+        // (this part adds: a linear layer's operands come while it does)
+        if constexpr (kEpi == kEpiLinear) out.ask(p, row0, col0 + c);
         __threadfence();  // the other parts' partials, counted in, are read after the count
         // 0 + p_0 + ... + p_{n-1}: the others' partials come two loads ahead
         // of the add; this part's own term (in registers) at its place
@@ -1029,6 +1035,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kCS) cluster_sync();  // every CTA's barriers initialised before any uses them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    griddep_launch();
+    griddep_wait();
     WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
     // work slot and, for the cluster split, this CTA's half of every tile's K
     const uint32_t cs_rank = kCS ? cluster_ctarank() : 0u;

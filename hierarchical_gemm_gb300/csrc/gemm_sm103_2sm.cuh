@@ -105,6 +105,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // barriers of every CTA initialised before any uses them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    griddep_launch();
+    griddep_wait();
     WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
     ctl.peer_abort[ctl.npeers++] = mapa_shared(smem_u32(const_cast<int*>(abort_flag)), half ^ 1u);
 

@@ -21,6 +21,17 @@ __device__ __forceinline__ uint64_t globaltimer() {
     return t;
 }
 
+// ------------------------------------------------- dependent launches --
+
+// A kernel launched as a programmatic dependent of the one before it in its
+// stream may start while that one still runs, once each of its blocks has
+// called griddep_launch() or ended; griddep_wait() returns when the earlier
+// kernel has completed and its writes are visible, and comes before the
+// first access to global memory.  Launched in the ordinary way, both do
+// nothing.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------- cluster --
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
