@@ -9,6 +9,8 @@
 // 2 + 8 + 4 for the gated one, against a few dozen flops, so HBM bounds
 // them.  A thread holds 8 neighbouring columns (16 bytes of a 16-bit row, a
 // warp 512 contiguous bytes) and walks down rows.
+#include <algorithm>
+
 #include "ffn_epilogue.cuh"
 #include "ffn_kernels.h"
 
@@ -18,6 +20,7 @@ namespace {
 
 constexpr int kStripCols = 256;  // columns of a thread block: 32 threads of 8
 constexpr int kRowLanes = 8;     // rows in flight per block
+constexpr int kLinearPerSM = 4, kGatedPerSM = 3;  // resident blocks
 
 // 8 fp32 values to the 16-bit row at p, columns [i, i + 8) of n.
 template <bool kBF16>
@@ -43,8 +46,13 @@ __device__ __forceinline__ int64_t chunk_begin(int64_t M, int64_t y, int64_t Y) 
 // 8 row lanes in lane order), the strip's blocks leave their sums in
 // `partials`, and the last of them to arrive adds them in chunk order, so
 // the bits do not depend on which block that is.
+//
+// Four blocks an SM (their 64 registers a thread just hold one row's
+// vectors): 4096 x 16384 bf16, gelu, sums alone, 85 us; with 3 blocks 110,
+// with 5 91, and with two rows in flight a thread 114 to 129, whatever the
+// vector's width.
 template <bool kBF16, int kAct>
-__global__ void __launch_bounds__(256) linear_grad_sm103(const LinearGradArgs a, const ColumnSums sums) {
+__global__ void __launch_bounds__(256, kLinearPerSM) linear_grad_sm103(const LinearGradArgs a, const ColumnSums sums) {
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kStripCols + tx * 8;
     const int64_t r1 = chunk_begin(a.M, blockIdx.y + 1, gridDim.y);
@@ -92,8 +100,17 @@ __global__ void __launch_bounds__(256) linear_grad_sm103(const LinearGradArgs a,
         if (!is_last) return;
         __threadfence();
         total = 0.0f;
-        if (c < a.N)
-            for (int64_t y = 0; y < gridDim.y; ++y) total += __ldcg(sums.partials + y * a.N + c);
+        if (c < a.N) {
+            // (8 loads in flight; the sum is in chunk order all the same)
+            const float* p = sums.partials + c;
+            for (int64_t y = 0; y < gridDim.y; y += 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = y + k < gridDim.y ? __ldcg(p + (y + k) * a.N) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) total += v[k];
+            }
+        }
         if (threadIdx.x == 0) sums.counters[blockIdx.x] = 0;  // ready for the next launch
     }
     if (c < a.N) {
@@ -105,7 +122,7 @@ __global__ void __launch_bounds__(256) linear_grad_sm103(const LinearGradArgs a,
 }
 
 template <bool kBF16, int kAct>
-__global__ void __launch_bounds__(256) gated_grad_sm103(const GatedGradArgs a) {
+__global__ void __launch_bounds__(256, kGatedPerSM) gated_grad_sm103(const GatedGradArgs a) {
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kStripCols + tx * 8;
     griddep_launch();
@@ -155,25 +172,41 @@ cudaError_t launch_grid(void (*kernel)(Args...), int64_t strips, int64_t chunks,
     lc.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(chunks), 1);
     lc.blockDim = dim3(256, 1, 1);
     lc.stream = stream;
-    cudaLaunchAttribute attr = dependent_launch();
-    lc.attrs = &attr;
-    lc.numAttrs = 1;
+    // The products before and after take most of an SM's shared memory: the
+    // same split of it between shared memory and cache spares every SM a
+    // change of it at both ends.
+    cudaLaunchAttribute attr[2] = {dependent_launch(), {}};
+    attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    attr[1].val.sharedMemCarveout = 100;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
     return cudaLaunchKernelEx(&lc, kernel, args...);
 }
 
-// Row chunks: enough blocks for 8 per SM, at least 32 rows a chunk.
-int64_t row_chunks(int64_t M, int64_t strips, int num_sms) {
-    const int64_t want = (static_cast<int64_t>(num_sms) * 8 + strips - 1) / strips;
-    const int64_t most = (M + 31) / 32;
-    const int64_t y = want < most ? want : most;
-    return y < 1 ? 1 : (y > 65535 ? 65535 : y);
+// Row chunks: as many as fill the `slots` blocks that can be resident in
+// whole rounds (the fewest that fill nine tenths of them, or else those that
+// fill most), of 16 rows at least.
+int64_t row_chunks(int64_t M, int64_t strips, int64_t slots) {
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>((M + 15) / 16, 65535));
+    int64_t best = 1;
+    double fill = 0.0;
+    for (int64_t y = 1; y <= most && strips * y <= 4 * slots; ++y) {
+        const int64_t blocks = strips * y, rounds = (blocks + slots - 1) / slots;
+        const double f = static_cast<double>(blocks) / static_cast<double>(rounds * slots);
+        if (f > fill) {
+            fill = f;
+            best = y;
+        }
+        if (f >= 0.9) break;
+    }
+    return best;
 }
 
 }  // namespace
 
 cudaError_t launch_linear_grad(const LinearGradArgs& a, const ColumnSums& sums, int num_sms, cudaStream_t stream) {
     const int64_t strips = (a.N + kStripCols - 1) / kStripCols;
-    int64_t y = row_chunks(a.M, strips, num_sms);
+    int64_t y = row_chunks(a.M, strips, static_cast<int64_t>(num_sms) * kLinearPerSM);
     if (a.dbias) {
         // the partials and counters have to fit; one chunk needs neither
         if (y * a.N > sums.partial_floats) y = sums.partial_floats / a.N;
@@ -186,7 +219,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const ColumnSums& sums, 
 
 cudaError_t launch_gated_grad(const GatedGradArgs& a, int num_sms, cudaStream_t stream) {
     const int64_t strips = (a.F + kStripCols - 1) / kStripCols;
-    const int64_t y = row_chunks(a.M, strips, num_sms);
+    const int64_t y = row_chunks(a.M, strips, static_cast<int64_t>(num_sms) * kLinearPerSM);
     return by_act(a.bf16, a.act, [&](auto b, auto act) {
         return launch_grid(&gated_grad_sm103<decltype(b)::value, decltype(act)::value>, strips, y, stream, a);
     });
