@@ -143,7 +143,18 @@ tsgemm_status_t make_config(tsffn_s* h, int kind, int64_t M, int64_t N, int64_t 
     tsgemm_status_t st =
         tsg::choose_config(Mp, round8(N), round8(K), din, dout, layout, h->num_sms, nullptr, &f.cfg, widths);
     if (st != TSGEMM_OK) return st;
-    if (f.cfg.workspace_bytes > kWorkspaceBytes || counters_of(f.cfg) > kCounters) {
+    // Whole tiles only where there is at least a round of them, and where the
+    // workspace does not hold the parts of cut ones.  With an epilogue, whose
+    // work falls to whichever part comes last while the others wait for no
+    // one, cutting the last tiles along K costs more than the even finish
+    // gives (linear with everything, stream-K against whole tiles: 1536 x
+    // 4096 x 4096, 1.26 rounds, 69 / 52 us; 4096 x 6144 x 2048, 5.05 rounds, 98
+    // / 86; 4096^3, 3.37 rounds, 107 / 101; gated save 52 / 49, 83 / 80, 97 /
+    // 96).
+    const bool cut = f.cfg.splits > 1 || f.cfg.stream_k_tiles > 0;
+    const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
+    if ((cut && kind != tsg::kEpiPlain && pair_tiles >= h->num_sms / 2) ||
+        f.cfg.workspace_bytes > kWorkspaceBytes || counters_of(f.cfg) > kCounters) {
         tsgemm_config_t whole{};
         whole.splits = 1;
         whole.stream_k_tiles = -1;

@@ -26,8 +26,8 @@ namespace tsg {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kVecsPerThread = 4;                                       // groups of 8 values
-constexpr int64_t kChunk = int64_t{kClipThreads} * kVecsPerThread * 8;  // values of a chunk: 8192
+constexpr int kVecsPerThread = 8;                                       // groups of 8 values
+constexpr int64_t kChunk = int64_t{kClipThreads} * kVecsPerThread * 8;  // values of a chunk: 16384
 constexpr int kFewTensors = 64, kMaxTensors = 512;                      // of a list
 
 // A list of tensors, cut into chunks.
@@ -143,59 +143,66 @@ __device__ __forceinline__ void add_squares(const float (&x)[8], float& s, doubl
     }
 }
 
-// This thread's groups of 8 values in chunk c, handed to f.  kLast: they are
-// not read again, so L2 need not keep them.
-template <bool kLast, class Table, class F>
-__device__ __forceinline__ void with_chunk(const Table& t, int64_t c, F&& f) {
+// Calls f(x, i) for this thread's groups of 8 values in chunk c, x the values
+// and i the index of the first; begin(tensor index, kind, aligned, n) tells
+// beforehand whose they are.  A whole chunk of 16-bit values: 128 bytes a
+// thread are asked for before the first is used.  kLast: the values are not
+// read again, so L2 need not keep them.
+template <bool kLast, class Table, class Begin, class F>
+__device__ __forceinline__ void with_chunk(const Table& t, int64_t c, Begin&& begin, F&& f) {
     const int k = tensor_of(t, c);
     const int kind = t.kind[k] & 0x7f;
     const bool aligned = t.kind[k] & 0x80;
     const int64_t n = t.numel[k], start = (c - t.first[k]) * kChunk, at = start + threadIdx.x * 8;
-    float x[kVecsPerThread][8];
+    begin(k, kind, aligned, n);
     if (aligned && start + kChunk <= n && kind != kElemF32) {
-        // a whole chunk of 16-bit values: every load before the first use
         uint4 w[kVecsPerThread];
 #pragma unroll
-        for (int v = 0; v < kVecsPerThread; ++v)
-        {
+        for (int v = 0; v < kVecsPerThread; ++v) {
             const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.in[k]) + at) + v * kClipThreads;
             w[v] = kLast ? __ldcs(p) : *p;
         }
 #pragma unroll
         for (int v = 0; v < kVecsPerThread; ++v) {
             const uint32_t r[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+            float x[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 y = kind == kElemBF16 ? unpack16<true>(r[j]) : unpack16<false>(r[j]);
-                x[v][2 * j] = y.x;
-                x[v][2 * j + 1] = y.y;
+                x[2 * j] = y.x;
+                x[2 * j + 1] = y.y;
             }
+            f(x, at + v * (kClipThreads * 8));
         }
     } else {
-#pragma unroll
+#pragma unroll 2
         for (int v = 0; v < kVecsPerThread; ++v) {
             const int64_t i = at + v * (kClipThreads * 8);
-            if (i < n) {
-                load8_any(kind, aligned, t.in[k], i, n, x[v]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[v][j] = 0.0f;
-            }
+            if (i >= n) break;
+            float x[8];
+            load8_any(kind, aligned, t.in[k], i, n, x);
+            f(x, i);
         }
     }
-    f(x, k, kind, aligned, at, n);
 }
+
+constexpr int kFp32Groups = 4;  // groups of 8 squares that an fp32 sum takes
 
 template <class Table>
 __device__ __forceinline__ double sum_chunks(const Table& t) {
     double acc = 0.0;
     for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        with_chunk<false>(t, c, [&](const float (&x)[kVecsPerThread][8], int, int, bool, int64_t, int64_t) {
-            float s = 0.0f;
-#pragma unroll
-            for (int v = 0; v < kVecsPerThread; ++v) add_squares(x[v], s, acc);
-            acc += static_cast<double>(s);
-        });
+        float s = 0.0f;
+        int groups = 0;
+        with_chunk<false>(t, c, [](int, int, bool, int64_t) {},
+                          [&](const float (&x)[8], int64_t) {
+                              add_squares(x, s, acc);
+                              if (++groups % kFp32Groups == 0) {
+                                  acc += static_cast<double>(s);
+                                  s = 0.0f;
+                              }
+                          });
+        acc += static_cast<double>(s);
     }
     return block_sum(acc);
 }
@@ -206,16 +213,21 @@ __device__ __forceinline__ void scale_chunks(const Table& t, float f) {
     if (t.chunks <= blockIdx.x) return;
     const int64_t last = blockIdx.x + (t.chunks - 1 - blockIdx.x) / gridDim.x * gridDim.x;
     for (int64_t c = last; c >= 0; c -= gridDim.x) {
-        with_chunk<true>(t, c, [&](float (&x)[kVecsPerThread][8], int k, int kind, bool aligned, int64_t at, int64_t n) {
+        int k = 0, kind = 0;
+        bool aligned = false;
+        int64_t n = 0;
+        with_chunk<true>(t, c,
+                         [&](int k_, int kind_, bool aligned_, int64_t n_) {
+                             k = k_;
+                             kind = kind_;
+                             aligned = aligned_;
+                             n = n_;
+                         },
+                         [&](float (&x)[8], int64_t i) {
 #pragma unroll
-            for (int v = 0; v < kVecsPerThread; ++v) {
-                const int64_t i = at + v * (kClipThreads * 8);
-                if (i >= n) break;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[v][j] *= f;
-                store8_any(kind, aligned, t.out[k], i, n, x[v]);
-            }
-        });
+                             for (int j = 0; j < 8; ++j) x[j] *= f;
+                             store8_any(kind, aligned, t.out[k], i, n, x);
+                         });
     }
 }
 

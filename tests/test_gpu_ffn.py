@@ -159,12 +159,45 @@ def test_gated_activations(ff, act, dtype, M):
     check_gated(ff, M, 200, 144, act=act, dtype=dtype, train=True, seed=3, pad=8)
 
 
+@pytest.mark.parametrize("rcr", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 33), (8, 129, 250), (12, 300, 1000), (16, 16, 4111), (17, 136, 520),
+                                   (24, 1031, 77), (31, 260, 2056), (32, 512, 512), (33, 512, 512), (2, 5200, 96),
+                                   (10, 9000, 72), (1, 2048, 2048), (20, 1544, 1544)])
+def test_few_rows(ff, M, N, K, rcr):
+    # 1, 2 and 4 groups of 8 rows, K split over 1 to 8 blocks of a cluster,
+    # more strips of columns than SMs, ragged ends of every kind
+    check_linear(ff, M, N, K, rcr, act="silu", bias=BF, residual=True, pad=8, seed=M * 31 + N)
+    check_gated(ff, M, max(8, N // 8 * 8), K, rcr, pad=8, train=M % 2 == 1, seed=M * 31 + N)
+
+
+def test_few_rows_ignore_what_lies_outside(ff):
+    # NaN in the padding of every row, in W's rows past N and in X's past M:
+    # products of them with zeros would be NaN
+    g = _gen(22)
+    for M, N, K in [(1, 33, 37), (5, 129, 250), (12, 70, 1003), (30, 136, 72)]:
+        for rcr in (False, True):
+            def guarded(r, c):
+                t = torch.full((r + 9, (c + 7) // 8 * 8 + 16), float("nan"), dtype=BF, device="cuda")
+                t[:r, :c] = torch.randn((r, c), generator=g, device="cuda").to(BF)
+                return t[:r, :c]
+            x = guarded(M, K)
+            w = guarded(N, K).t() if rcr else guarded(K, N)
+            want = ref.linear(ref.f64(x), ref.f64(w), None, "none", None, BF)
+            C, _ = ff.linear(x, w, save=True)
+            ref.check(C, want["c"], "C")
+            F = N // 16 * 8
+            wg = guarded(2 * F, K).t() if rcr else guarded(K, 2 * F)
+            want = ref.gated(ref.f64(x), ref.f64(wg), "silu", BF)
+            ref.check(ff.gated(x, wg), want["h"], "H")
+
+
 def _sampled(M, n, seed):
     return np.sort(np.random.default_rng(seed).choice(M, n, replace=False))
 
 
 @pytest.mark.parametrize("rcr", [False, True])
-@pytest.mark.parametrize("M,N,K", [(5100, 9712, 200),   # 256 x 512 pair tiles, five rounds
+@pytest.mark.parametrize("M,N,K", [(2000, 2608, 72),    # 256-wide pair tiles, a round and a bit
+                                   (5100, 9712, 200),   # 256 x 512 pair tiles, five rounds
                                    (2300, 2192, 520)])  # 256-wide pair tiles with a ragged edge
 def test_large_tiles(ff, M, N, K, rcr):
     # sampled rows against the reference (a row of C depends on its row of X)
