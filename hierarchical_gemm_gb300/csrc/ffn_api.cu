@@ -161,10 +161,28 @@ tsgemm_status_t make_config(tsffn_s* h, int kind, int64_t M, int64_t N, int64_t 
         st = tsg::choose_config(Mp, round8(N), round8(K), din, dout, layout, h->num_sms, &whole, &f.cfg, widths);
         if (st != TSGEMM_OK) return st;
     }
+    // 256 x 512 tiles beyond the planner's own choice of them: for long K they
+    // pay with fewer than four rounds too, as long as the rounds are mostly
+    // full (us, 256 x 256 / 256 x 512: 4096 x 4096 x 16384, 1.68 rounds, 390 /
+    // 317; 4096 x 4096 x 28672 625 / 563; 2048 x 2048 x 10928, 0.42 rounds, 59 /
+    // 106), and the weight gradient's layout has them as well.
+    const int64_t wide_slots = h->num_sms / 2, wide_tiles = ((M + 255) / 256) * ((N + 511) / 512);
+    const int64_t rounds = (wide_tiles + wide_slots - 1) / wide_slots;
+    if (f.cfg.block_n != 512 && N >= 512 && 5 * wide_tiles >= 4 * rounds * wide_slots &&
+        (K >= 8192 || (rounds >= 4 && layout == TSGEMM_LAYOUT_CRR))) {
+        tsgemm_config_t wide{};
+        wide.block_m = 256;
+        wide.block_n = 512;
+        tsgemm_config_t c{};
+        if (tsg::choose_config(Mp, round8(N), round8(K), din, dout, layout, h->num_sms, &wide, &c) == TSGEMM_OK) f.cfg = c;
+    }
     const bool pair = f.cfg.block_m == 256;
-    f.kernel = kernel_of(kind, layout, f.cfg, out_kind(dout));
+    // (the plain kernels have no 256 x 512 form for that layout; the linear
+    // layer's with nothing to do is one)
+    const int run_as = kind == tsg::kEpiPlain && f.cfg.block_n == 512 && layout == TSGEMM_LAYOUT_CRR ? tsg::kEpiLinear : kind;
+    f.kernel = kernel_of(run_as, layout, f.cfg, out_kind(dout));
     const int64_t need = tsg::smem_bytes_for(f.cfg.block_m, f.cfg.block_n, dout, f.cfg.stages, 1) +
-                         (kind == tsg::kEpiLinear ? static_cast<int64_t>(tsg::kResidBarBytes) : 0);
+                         (run_as == tsg::kEpiLinear ? static_cast<int64_t>(tsg::kResidBarBytes) : 0);
     if (!f.kernel || need > tsg::kSmemPerCtaMax) return TSGEMM_ERR_UNSUPPORTED;
     // (more than half the SM's shared memory, so one CTA owns each SM and
     // its tensor memory)

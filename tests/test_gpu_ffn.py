@@ -221,6 +221,31 @@ def test_large_tiles(ff, M, N, K, rcr):
 
 
 @pytest.mark.parametrize("rcr", [False, True])
+def test_large_products_of_the_backward_pass(ff, rcr):
+    # 256 x 512 tiles for a long contraction (dX) and for the weight
+    # gradient's layout (dW), sampled rows against the reference
+    g = _gen(12)
+    M, N, K = 4100, 8200, 4088
+    x, w = rows(M, K, BF, g), weights(K, N, rcr, BF, g)
+    dc = rows(M, N, BF, g)
+    dx, dw, _ = ff.linear_backward(dc, x, w)
+    torch.cuda.synchronize()
+    assert ff.status() == 0
+    at = _sampled(M, 12, 2)
+    d64, w64 = ref.f64(dc[at]), ref.f64(w)
+    v, e = ref.product(d64, w64.T)
+    ref.check(dx[at], (v, ref.rounded(v, e, BF)), "dX")
+    M, N, K = 1030, 9720, 9736
+    x, w = rows(M, K, BF, g), weights(K, N, rcr, BF, g)
+    dc = rows(M, N, BF, g)
+    _, dw, _ = ff.linear_backward(dc, x, w, need=("dW",))
+    at = _sampled(K, 12, 3)
+    v, e = ref.product(ref.f64(x).T[at], ref.f64(dc))
+    ref.check(dw[at], (v, ref.rounded(v, e, BF)), "dW")
+    assert bool(torch.isfinite(dw.float()).all()) and ff.status() == 0
+
+
+@pytest.mark.parametrize("rcr", [False, True])
 def test_integers_are_exact(ff, rcr):
     # integer operands whose sums fp32 holds: one rounding, so equal bits
     g = _gen(12)
