@@ -412,9 +412,16 @@ tsgemm_status_t check_device_ptr(const void* p, int device) {
 // before the handle is looked at): types, the matrices that are present
 // (inputs first, then outputs), no output on anything else (but `alias`,
 // which may be the first output exactly).
+struct Mats {
+    Mat m[5];
+    int n = 0;
+    void add(const Mat& x) { m[n++] = x; }
+    const Mat* begin() const { return m; }
+    const Mat* end() const { return m + n; }
+};
 struct Call {
     int dtype, layout, act;
-    std::vector<Mat> in, out;
+    Mats in, out;
     Mat alias{};  // present when .p is set
 };
 
@@ -434,13 +441,14 @@ tsgemm_status_t check_call(const Call& c) {
         const tsgemm_status_t st = check_mat(c.alias);
         if (st != TSGEMM_OK) return st;
     }
-    for (size_t i = 0; i < c.out.size(); ++i) {
+    for (int i = 0; i < c.out.n; ++i) {
+        const Mat& o = c.out.m[i];
         for (const Mat& m : c.in)
-            if (overlaps(c.out[i], m)) return TSGEMM_ERR_INVALID_ARG;
-        for (size_t j = 0; j < i; ++j)
-            if (overlaps(c.out[i], c.out[j])) return TSGEMM_ERR_INVALID_ARG;
-        const bool same = i == 0 && c.alias.p == c.out[0].p && c.alias.ld == c.out[0].ld;
-        if (!same && overlaps(c.out[i], c.alias)) return TSGEMM_ERR_INVALID_ARG;
+            if (overlaps(o, m)) return TSGEMM_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(o, c.out.m[j])) return TSGEMM_ERR_INVALID_ARG;
+        const bool same = i == 0 && c.alias.p == o.p && c.alias.ld == o.ld;
+        if (!same && overlaps(o, c.alias)) return TSGEMM_ERR_INVALID_ARG;
     }
     return TSGEMM_OK;
 }
@@ -612,10 +620,11 @@ tsgemm_status_t tsffn_linear(tsffn_t h, const tsffn_linear_args* a, void* stream
     return guarded([&]() -> tsgemm_status_t {
         const int64_t eo = elem_bytes(a->dtype_out), eb = elem_bytes(a->dtype_bias);
         Call c{a->dtype, a->layout, a->act, {}, {}, {}};
-        c.in = {{a->X, a->M, a->K, a->ldx, 2},
-                weights(a->W, a->layout, a->N, a->K, a->ldw, 2),
-                {a->bias, 1, a->N, round8(a->N), eb}};
-        c.out = {{a->C, a->M, a->N, a->ldc, eo}, {a->saved, a->M, a->N, TSFFN_SAVED_LD(a->N), 4}};
+        c.in.add({a->X, a->M, a->K, a->ldx, 2});
+        c.in.add(weights(a->W, a->layout, a->N, a->K, a->ldw, 2));
+        c.in.add({a->bias, 1, a->N, round8(a->N), eb});
+        c.out.add({a->C, a->M, a->N, a->ldc, eo});
+        c.out.add({a->saved, a->M, a->N, TSFFN_SAVED_LD(a->N), 4});
         if (a->residual) c.alias = {a->residual, a->M, a->N, a->ldr, eo};
         tsgemm_status_t st = check_call(c);
         if (st == TSGEMM_OK) st = check_out_type(a->dtype_out, a->dtype);
@@ -649,15 +658,14 @@ tsgemm_status_t tsffn_linear_backward(tsffn_t h, const tsffn_linear_backward_arg
     return guarded([&]() -> tsgemm_status_t {
         const int64_t ldz = TSFFN_SAVED_LD(a->N);
         Call c{a->dtype, a->layout, a->act, {}, {}, {}};
-        c.in = {{a->dC, a->M, a->N, a->lddc, 2}};
-        if (a->dW) c.in.push_back({a->X, a->M, a->K, a->ldx, 2});
-        if (a->dX) c.in.push_back(weights(a->W, a->layout, a->N, a->K, a->ldw, 2));
-        if (grad) c.in.push_back({a->saved, a->M, a->N, ldz, 4});
-        const Mat dw = weights(a->dW, a->layout, a->N, a->K, a->lddw, elem_bytes(a->dtype_dw));
-        c.out = {{a->dX, a->M, a->K, a->lddx, 2},
-                 dw,
-                 {a->dbias, 1, a->N, ldz, elem_bytes(a->dtype_bias)},
-                 {grad && products ? a->workspace : nullptr, a->M, a->N, ldz, 2}};
+        c.in.add({a->dC, a->M, a->N, a->lddc, 2});
+        if (a->dW) c.in.add({a->X, a->M, a->K, a->ldx, 2});
+        if (a->dX) c.in.add(weights(a->W, a->layout, a->N, a->K, a->ldw, 2));
+        if (grad) c.in.add({a->saved, a->M, a->N, ldz, 4});
+        c.out.add({a->dX, a->M, a->K, a->lddx, 2});
+        c.out.add(weights(a->dW, a->layout, a->N, a->K, a->lddw, elem_bytes(a->dtype_dw)));
+        c.out.add({a->dbias, 1, a->N, ldz, elem_bytes(a->dtype_bias)});
+        c.out.add({grad && products ? a->workspace : nullptr, a->M, a->N, ldz, 2});
         tsgemm_status_t st = check_call(c);
         if (st == TSGEMM_OK && a->dW) st = check_out_type(a->dtype_dw, a->dtype);
         if (st == TSGEMM_OK && a->dbias) st = check_out_type(a->dtype_bias, a->dtype);
@@ -699,8 +707,10 @@ tsgemm_status_t tsffn_gated(tsffn_t h, const tsffn_gated_args* a, void* stream) 
     if (sizes != TSGEMM_OK) return sizes;
     return guarded([&]() -> tsgemm_status_t {
         Call c{a->dtype, a->layout, a->act, {}, {}, {}};
-        c.in = {{a->X, a->M, a->K, a->ldx, 2}, weights(a->W, a->layout, 2 * a->F, a->K, a->ldw, 2)};
-        c.out = {{a->H, a->M, a->F, a->ldh, 2}, {a->saved, a->M, 2 * a->F, 2 * a->F, 4}};
+        c.in.add({a->X, a->M, a->K, a->ldx, 2});
+        c.in.add(weights(a->W, a->layout, 2 * a->F, a->K, a->ldw, 2));
+        c.out.add({a->H, a->M, a->F, a->ldh, 2});
+        c.out.add({a->saved, a->M, 2 * a->F, 2 * a->F, 4});
         tsgemm_status_t st = check_call(c);
         if (st == TSGEMM_OK) st = check_memory(h, c);
         if (st != TSGEMM_OK) return st;
@@ -723,11 +733,13 @@ tsgemm_status_t tsffn_gated_backward(tsffn_t h, const tsffn_gated_backward_args*
     return guarded([&]() -> tsgemm_status_t {
         const int64_t N = 2 * a->F;
         Call c{a->dtype, a->layout, a->act, {}, {}, {}};
-        c.in = {{a->dH, a->M, a->F, a->lddh, 2}, {a->saved, a->M, N, N, 4}};
-        if (a->dW) c.in.push_back({a->X, a->M, a->K, a->ldx, 2});
-        if (a->dX) c.in.push_back(weights(a->W, a->layout, N, a->K, a->ldw, 2));
-        const Mat dw = weights(a->dW, a->layout, N, a->K, a->lddw, elem_bytes(a->dtype_dw));
-        c.out = {{a->dX, a->M, a->K, a->lddx, 2}, dw, {a->workspace, a->M, N, N, 2}};
+        c.in.add({a->dH, a->M, a->F, a->lddh, 2});
+        c.in.add({a->saved, a->M, N, N, 4});
+        if (a->dW) c.in.add({a->X, a->M, a->K, a->ldx, 2});
+        if (a->dX) c.in.add(weights(a->W, a->layout, N, a->K, a->ldw, 2));
+        c.out.add({a->dX, a->M, a->K, a->lddx, 2});
+        c.out.add(weights(a->dW, a->layout, N, a->K, a->lddw, elem_bytes(a->dtype_dw)));
+        c.out.add({a->workspace, a->M, N, N, 2});
         tsgemm_status_t st = check_call(c);
         if (st == TSGEMM_OK && a->dW) st = check_out_type(a->dtype_dw, a->dtype);
         if (st == TSGEMM_OK) st = check_memory(h, c);

@@ -184,15 +184,18 @@ cudaError_t launch_grid(void (*kernel)(Args...), int64_t strips, int64_t chunks,
 }
 
 // Row chunks: as many as fill the `slots` blocks that can be resident in
-// whole rounds (the fewest that fill nine tenths of them, or else those that
-// fill most), of 16 rows at least.
-int64_t row_chunks(int64_t M, int64_t strips, int64_t slots) {
+// `rounds` whole rounds or a few more (the fewest that fill nine tenths of
+// them, or else those that fill most), of 16 rows at least.  Several rounds
+// keep the rows being read at any time close together: gated 4096 x 14336,
+// one round 183 us, three 140; the linear layer, whose chunks cost
+// partial sums, is as fast with two as with one.
+int64_t row_chunks(int64_t M, int64_t strips, int64_t slots, int64_t rounds) {
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>((M + 15) / 16, 65535));
-    int64_t best = 1;
+    int64_t best = std::min(most, std::max<int64_t>(1, (rounds - 1) * slots / strips));
     double fill = 0.0;
-    for (int64_t y = 1; y <= most && strips * y <= 4 * slots; ++y) {
-        const int64_t blocks = strips * y, rounds = (blocks + slots - 1) / slots;
-        const double f = static_cast<double>(blocks) / static_cast<double>(rounds * slots);
+    for (int64_t y = best; y <= most && strips * y <= (rounds + 3) * slots; ++y) {
+        const int64_t blocks = strips * y, full = (blocks + slots - 1) / slots * slots;
+        const double f = static_cast<double>(blocks) / static_cast<double>(full);
         if (f > fill) {
             fill = f;
             best = y;
@@ -206,7 +209,7 @@ int64_t row_chunks(int64_t M, int64_t strips, int64_t slots) {
 
 cudaError_t launch_linear_grad(const LinearGradArgs& a, const ColumnSums& sums, int num_sms, cudaStream_t stream) {
     const int64_t strips = (a.N + kStripCols - 1) / kStripCols;
-    int64_t y = row_chunks(a.M, strips, static_cast<int64_t>(num_sms) * kLinearPerSM);
+    int64_t y = row_chunks(a.M, strips, static_cast<int64_t>(num_sms) * kLinearPerSM, 2);
     if (a.dbias) {
         // the partials and counters have to fit; one chunk needs neither
         if (y * a.N > sums.partial_floats) y = sums.partial_floats / a.N;
@@ -219,7 +222,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, const ColumnSums& sums, 
 
 cudaError_t launch_gated_grad(const GatedGradArgs& a, int num_sms, cudaStream_t stream) {
     const int64_t strips = (a.F + kStripCols - 1) / kStripCols;
-    const int64_t y = row_chunks(a.M, strips, static_cast<int64_t>(num_sms) * kLinearPerSM);
+    const int64_t y = row_chunks(a.M, strips, static_cast<int64_t>(num_sms) * kGatedPerSM, 3);
     return by_act(a.bf16, a.act, [&](auto b, auto act) {
         return launch_grid(&gated_grad_sm103<decltype(b)::value, decltype(act)::value>, strips, y, stream, a);
     });

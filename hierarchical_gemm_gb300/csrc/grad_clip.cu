@@ -235,6 +235,7 @@ __device__ __forceinline__ void scale_chunks(const Table& t, float f) {
 __device__ __forceinline__ float clip_coef(double sum, float max_norm, float* norm) {
     const double n = sqrt(sum);
     if (norm) *norm = static_cast<float>(n);
+    if (isinf(max_norm)) return 1.0f;  // the norm alone, whatever it is
     double f = static_cast<double>(max_norm) / (n + 1e-6);
     if (f > 1.0) f = 1.0;  // (a NaN stays one)
     return static_cast<float>(f);

@@ -176,7 +176,8 @@ TSGEMM_API tsgemm_status_t tsffn_gated_backward(tsffn_t handle, const tsffn_gate
  * grads[i] * min(1, max_norm / (norm + 1e-6)), *norm (a device float) the
  * norm.  A norm that is not finite takes its course through that formula.
  * Tensors need only be aligned to their own type; 16-byte aligned ones are
- * read in 16-byte vectors.  max_norm >= 0 (infinity: the norm alone). */
+ * read in 16-byte vectors.  max_norm >= 0 (infinity: the norm alone, nothing
+ * is scaled). */
 TSGEMM_API tsgemm_status_t tsffn_clip_grad_norm(tsffn_t handle, int64_t count, const void* const* grads,
                                                 void* const* out, const int64_t* numel, const int32_t* dtype,
                                                 float max_norm, float* norm, void* stream);

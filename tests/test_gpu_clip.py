@@ -127,6 +127,17 @@ def test_below_the_limit_nothing_changes(ff):
     assert all(torch.equal(a, b) for a, b in zip(g, keep))
 
 
+def test_the_norm_alone(ff):
+    # no limit: nothing changes, not even for a norm that is not finite
+    for extra in (0.0, math.inf, math.nan):
+        g = _tensors([1000, 77], [BF, FL], 9)
+        g[0][3] = extra
+        keep = [t.clone() for t in g]
+        norm = float(ff.clip_grad_norm(g, math.inf))
+        assert math.isfinite(norm) == math.isfinite(extra)
+        assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(g, keep))
+
+
 def test_reproducible(ff):
     g = _tensors([1234567, 4097, 3], [BF, FL, HF], 8)
     one = float(ff.clip_grad_norm(g, 1.0, out=[torch.empty_like(t) for t in g]))
