@@ -153,11 +153,21 @@ tsgemm_status_t make_config(tsffn_s* h, int kind, int64_t M, int64_t N, int64_t 
     // 96).
     const bool cut = f.cfg.splits > 1 || f.cfg.stream_k_tiles > 0;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
-    if ((cut && kind != tsg::kEpiPlain && pair_tiles >= h->num_sms / 2) ||
+    // A linear layer's 256 x 512 tiles cannot hide their epilogue behind the
+    // next tile (both accumulators are taken), which a short contraction does
+    // not make up for: 256 x 256 below K = 8192 (the training step of a 4096 x
+    // 16384 x 4096 layer 1133 us against 1155).  The gated layer stores half as
+    // much a tile and keeps them (4096 x 14336 x 4096 552 against 577).
+    const bool narrow = kind == tsg::kEpiLinear && f.cfg.block_n == 512 && K < 8192;
+    if ((cut && kind != tsg::kEpiPlain && pair_tiles >= h->num_sms / 2) || narrow ||
         f.cfg.workspace_bytes > kWorkspaceBytes || counters_of(f.cfg) > kCounters) {
         tsgemm_config_t whole{};
         whole.splits = 1;
         whole.stream_k_tiles = -1;
+        if (narrow) {
+            whole.block_m = 256;
+            whole.block_n = 256;
+        }
         st = tsg::choose_config(Mp, round8(N), round8(K), din, dout, layout, h->num_sms, &whole, &f.cfg, widths);
         if (st != TSGEMM_OK) return st;
     }
