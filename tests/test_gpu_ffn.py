@@ -196,7 +196,8 @@ def _sampled(M, n, seed):
 
 
 @pytest.mark.parametrize("rcr", [False, True])
-@pytest.mark.parametrize("M,N,K", [(2000, 2608, 72),    # 256-wide pair tiles, a round and a bit
+@pytest.mark.parametrize("M,N,K", [(1000, 8176, 8200),  # 256 x 512 pair tiles, part of a round, long K
+                                   (2000, 2608, 72),    # 256-wide pair tiles, a round and a bit
                                    (5100, 9712, 200),   # 256 x 512 pair tiles, five rounds
                                    (2300, 2192, 520)])  # 256-wide pair tiles with a ragged edge
 def test_large_tiles(ff, M, N, K, rcr):
@@ -345,6 +346,44 @@ def test_streams_and_handles(ff):
     assert torch.equal(ff.linear(x, w, act="silu", handle=h), want) and h.status() == 0
     torch.cuda.synchronize()
     h.close()
+
+
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_chain_without_waiting(ff, M):
+    # kernels of a chain start before the one before has ended: every buffer
+    # is written, read and written again along it, by them and by torch, and
+    # the result has the bits of a chain that waits after every call
+    g = _gen(23)
+    K, F = 512, 768
+    w1, w2 = weights(K, 2 * F, True, BF, g), weights(F, K, M == 20, BF, g)
+    x0 = rows(M, K, BF, g)
+    results = []
+    for wait in (True, False):
+        def step_over():
+            if wait:
+                torch.cuda.synchronize()
+        x, h, y = x0.clone(), unset(M, F, BF), unset(M, K, BF)
+        wa, out = w1.t().clone().t(), []
+        dw = torch.empty_like(wa)
+        for i in range(30):
+            _, saved = ff.gated(x, wa, H=h, save=True)
+            step_over()
+            ff.linear(h, w2, residual=x, C=y)
+            step_over()
+            dx, _ = ff.gated_backward(h, x, wa, saved, dW=dw)
+            step_over()
+            norm = ff.clip_grad_norm([dw.t()], 0.01)
+            step_over()
+            ff.linear(y, w2.t(), C=h, residual=h)
+            step_over()
+            wa.sub_(dw)
+            torch.mul(y, 0.5, out=x)
+            out.append((norm, dx, y.clone(), h.clone()))
+        torch.cuda.synchronize()
+        results.append(out)
+    for a, b in zip(*results):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert ff.status() == 0
 
 
 def test_graph_capture(ff):
