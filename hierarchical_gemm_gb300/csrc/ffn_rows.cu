@@ -15,7 +15,10 @@
 // each warp keeps a ring of 16-byte asynchronous copies of its own (no
 // block-wide barrier guards a slot) that runs ahead across strips, over
 // 100 KiB an SM in all.  The copies take a length, so the last partial
-// vectors of K and of the columns read as zeros past their end.
+// vectors of K and of the columns read as zeros past their end.  Measured, one
+// row, bf16, in a chain: 28672 x 4096 (N x K) 36 us, 6.5 TB/s, 0.96 of the
+// copy rate; 14336 x 8192 (K x N) 39; 4096 x 4096 7.2, where the launch is a
+// third (registers in place of the rings: 41, 50 and 12.6).
 //
 // The order of k within a fragment is free as long as W and X agree, so a
 // thread takes whole 16-byte vectors of W as they lie in memory:

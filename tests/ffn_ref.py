@@ -11,7 +11,8 @@ Where the bounds come from, per element:
     so (K / 16 + 2) 2^-21 S (a few-rows kernel, which rounds every addition,
     stays within K 2^-24 S, less than that);
   * the activations: ex2.approx and a fast division are within 2^-20
-    relative of the sigmoid, erfcf within 2^-21; so act(z) is within
+    relative of the sigmoid, and so is the normal distribution function
+    for |z| < 2; so act(z) is within
     2^-19 (|z| + 1) 2^-1 and act'(z) within 2^-18, on top of what an error
     in z makes of it: |act'| <= 1.13 and |act''| <= 1.2 for all of them but
     relu, whose derivative steps at 0 (values of z closer to 0 than their
