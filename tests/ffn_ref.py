@@ -8,8 +8,7 @@ Where the bounds come from, per element:
   * a sum of K products in the tensor cores: the products are exact, and
     each 16-deep step adds to a running fp32 sum, aligning and truncating:
     at most 4 units of 2^-23 of the sum of magnitudes S = sum |a b| per step,
-    so (K / 16 + 2) 2^-21 S (a few-rows kernel, which rounds every addition,
-    stays within K 2^-24 S, less than that);
+    so (K / 16 + 2) 2^-21 S (the few-rows kernels' fragments are 16 deep too);
   * the activations: ex2.approx and a fast division are within 2^-20
     relative of the sigmoid, and so is the normal distribution function
     for |z| < 2; so act(z) is within
