@@ -123,7 +123,7 @@ def test_linear_types(ff, dtype, out, bias, M, N):
     check_linear(ff, M, N, 192, False, dtype, "none", bias, False, out, seed=5)
 
 
-@pytest.mark.parametrize("M", [1, 4, 16, 130])
+@pytest.mark.parametrize("M", [1, 4, 16, 40, 130, 300])
 @pytest.mark.parametrize("rcr", [False, True])
 def test_long_k(ff, M, rcr):
     # few tiles and many K slices: the K split with its reduction
